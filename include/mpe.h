@@ -550,6 +550,136 @@ int mpe_prefix_read_layer(mpe_prefix* store, int32_t e, int32_t layer, void* hos
 /* mpe_prefix_get_absmax -- m_e of every expert (host float[E]). */
 int mpe_prefix_get_absmax(mpe_prefix* store, float* m_host);
 
+/* ------------------------------------------------------------------------
+ * Around the routed experts: the choice of experts that mpe_moe_ffn takes,
+ * the importances that the width rules take, and the dense products beside
+ * the experts (the router's projection, shared experts, projections added to
+ * the layer's output). These calls need no context and allocate nothing; they
+ * run on `stream` of the current device (every pointer belongs to it) and are
+ * asynchronous. A message for a refused call is in mpe_last_error_global. The
+ * first call on a device loads the library's kernels onto it, so make it
+ * before any stream capture. Calls may overlap on the GPU in any way as long
+ * as none writes what another reads or writes.
+ * ------------------------------------------------------------------------ */
+
+/* value types */
+#define MPE_TYPE_F32  0
+#define MPE_TYPE_BF16 1
+#define MPE_TYPE_F16  2
+
+/* scores of router logits l: e^l_e / sum_i e^l_i, or 1 / (1 + e^-l_e) */
+#define MPE_SCORE_SOFTMAX 0
+#define MPE_SCORE_SIGMOID 1
+
+/* a group's score: its largest key, or the sum of its two largest */
+#define MPE_GROUP_MAX  0
+#define MPE_GROUP_TOP2 1
+
+#define MPE_MAX_TOPK   32  /* experts chosen per token           */
+#define MPE_MAX_GROUPS 32  /* groups the choice can be limited to */
+
+typedef struct mpe_select_config {
+    int32_t E;            /* experts, 1 .. MPE_MAX_EXPERTS                                     */
+    int32_t k;            /* chosen per token, 1 .. MPE_MAX_TOPK, at most keep_groups E / n_groups */
+    int32_t score;        /* MPE_SCORE_*                                                       */
+    int32_t n_groups;     /* 1 .. MPE_MAX_GROUPS, divides E; expert e is in group e / (E / n_groups) */
+    int32_t keep_groups;  /* 1 .. n_groups                                                     */
+    int32_t group_score;  /* MPE_GROUP_* (unused when every group is kept)                     */
+    int32_t renormalize;  /* != 0: divide a token's weights by their sum                       */
+    float   scale;        /* factor of every weight                                            */
+} mpe_select_config;
+
+/*
+ * mpe_select_experts -- each token's experts and weights from its router
+ * logits, in the form mpe_moe_ffn takes. With scores s_e (MPE_SCORE_*) and
+ * keys s_e + bias_e: the keep_groups groups of highest group score are kept
+ * (all when keep_groups = n_groups), and the k experts of largest key in them
+ * are chosen, in descending order of key; ties go to the lower index, for
+ * groups too. The weight of a chosen expert is scale s_e, or
+ * scale s_e / (sum of the chosen s) with renormalize. Without a bias the order
+ * (of groups by MPE_GROUP_MAX too) is the logits' own.
+ * The choice is that of float64 scores and keys: float32 ones decide
+ * wherever they are further apart than their error. Weights are float32.
+ *   logits  device, [T x E] of `type` (MPE_TYPE_*), rows ld elements apart
+ *   T       tokens (>= 0), T k <= MPE_MAX_ASSIGNMENTS
+ *   bias    device, float32 [E], or NULL
+ *   ids     device, int32 [T x k]; w device, float32 [T x k]
+ * A logit of -inf has score 0 (masked), a bias of -inf bars an expert until
+ * nothing else is left, and a token whose chosen scores are all 0 gets weights
+ * 0 (with ids, as everywhere, in [0, E)). A NaN logit, or +inf under the
+ * softmax, gives its token NaN weights; NaN keys rank lowest.
+ * MPE_ERR_INVALID for a bad config, type, T, ld < E, a null pointer, or a
+ * pointer that is not aligned to its elements.
+ */
+int mpe_select_experts(const mpe_select_config* cfg, const void* logits, int32_t type, int64_t ld,
+                       int32_t T, const float* bias, int32_t* ids, float* w, void* stream);
+
+/*
+ * mpe_expert_importance -- the experts' importances p_e over a batch of
+ * tokens, as the width rules (mpe_allocate_bits, mpe_repage) take them: the
+ * mean routing score p_e = 1/T sum_t s_{t,e} (MPE_SCORE_*). The sums' order is
+ * fixed by T and E: the same input gives the same bits.
+ *   logits, type, ld, T as for mpe_select_experts, with T >= 1
+ *   p_out      device, float32 [E]
+ *   workspace  device, 16-byte aligned, at least
+ *              mpe_expert_importance_workspace(T, E) bytes (NULL when that is
+ *              0); written by the call, free again when the call has finished
+ * -inf logits score 0; a token of nothing else scores 0 for every expert. A
+ * NaN logit makes importances NaN (its expert's under the sigmoid, all of them
+ * under the softmax, as +inf does there). MPE_ERR_INVALID as for
+ * mpe_select_experts, and for a workspace that is too small.
+ */
+int mpe_expert_importance(const void* logits, int32_t type, int64_t ld, int32_t T, int32_t E,
+                          int32_t score, float* p_out, void* workspace, size_t workspace_bytes,
+                          void* stream);
+size_t mpe_expert_importance_workspace(int32_t T, int32_t E);
+
+/* activations of mpe_linear */
+#define MPE_ACT_NONE      0
+#define MPE_ACT_RELU      1  /* max(v, 0)                                            */
+#define MPE_ACT_SILU      2  /* v / (1 + e^-v)                                       */
+#define MPE_ACT_GELU      3  /* v (1 + erf(v / sqrt 2)) / 2                          */
+#define MPE_ACT_GELU_TANH 4  /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2    */
+
+typedef struct mpe_linear_args {
+    const void* x;         /* device, [M x K] of `type`, rows ldx elements apart              */
+    const void* w;         /* device, [N x K] of `type` (gated: [2N x K]), rows ldw apart      */
+    const void* bias;      /* device, [N] of `bias_type` (gated: [2N]), or NULL                */
+    const void* residual;  /* device, [M x N] of `out_type`, rows ldr elements apart, or NULL  */
+    void*       out;       /* device, [M x N] of `out_type`, rows ldo elements apart           */
+    int64_t ldx, ldw, ldr, ldo;
+    int32_t M, N, K;       /* M >= 0 tokens, N >= 1 outputs, K >= 1 inputs                     */
+    int32_t type;          /* MPE_TYPE_BF16 or MPE_TYPE_F16                                    */
+    int32_t bias_type;     /* `type` or MPE_TYPE_F32                                           */
+    int32_t out_type;      /* `type` or MPE_TYPE_F32                                           */
+    int32_t act;           /* MPE_ACT_*                                                        */
+    int32_t gated;         /* != 0: w's rows [0, N) are the gate's, [N, 2N) the up projection's */
+} mpe_linear_args;
+
+/*
+ * mpe_linear -- a dense product with its epilogue in one kernel:
+ *   out = act(x w^T + bias) + residual, or, gated,
+ *   out = act(x wg^T + bg) (x wu^T + bu) + residual,
+ * products accumulated and the epilogue computed in fp32, rounded once to
+ * out_type. The same input gives the same bits.
+ * x and w are 16-byte aligned with ldx and ldw multiples of 8 (a pitch of one
+ * row is not read and may be anything); bias, residual and out are aligned to
+ * their elements; ldx, ldw >= K, ldr, ldo >= N. `residual` may be `out` itself
+ * (same address and pitch); apart from that `out` must not overlap any input.
+ * M, N and K up to 2^30 each, pitches below 2^38.
+ * M = 0 does nothing. MPE_ERR_INVALID for anything else that breaks these
+ * rules; MPE_ERR_CUDA if the launch fails.
+ */
+int mpe_linear(const mpe_linear_args* args, void* stream);
+
+/*
+ * mpe_global_status -- synchronise the current device and return the sticky
+ * status word of the context-free calls on it (MPE_STATUS_WAIT_TIMEOUT: a
+ * bounded wait inside mpe_linear gave up, and its output is not to be used);
+ * clear it if `clear` != 0.
+ */
+int mpe_global_status(uint32_t* status_out, int32_t clear);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -35,6 +36,11 @@ STORE_DEVICE, STORE_HOST = 0, 1
 MAX_COMP_CHANNELS = 256
 ALLOC_STATE_CAP = 65536
 MAX_EXPERTS = 1024
+MAX_TOPK = 32
+TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 
 # every symbol include/mpe.h declares
 EXPORTS = [
@@ -49,6 +55,8 @@ EXPORTS = [
     "mpe_get_scales", "mpe_get_bits", "mpe_get_status", "mpe_last_error",
     "mpe_last_error_global", "mpe_kernel_launches", "mpe_version", "mpe_profile_enable",
     "mpe_profile_read", "mpe_route_noalloc", "mpe_moe_ffn_host_async", "mpe_host_wait",
+    "mpe_select_experts", "mpe_expert_importance", "mpe_expert_importance_workspace",
+    "mpe_linear", "mpe_global_status",
 ]
 PROFILE_SLOTS = ["route", "gate_up", "swiglu_reduce", "down", "combine", "tc_gate_up",
                  "tc_down", "tc_permute", "select", "compensate"]
@@ -90,6 +98,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, u32, u64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32,
                              ctypes.c_uint64, ctypes.c_size_t)
+    i64 = ctypes.c_int64
     sig = {
         "mpe_create": (i32, [ctypes.POINTER(vp), ctypes.POINTER(Config)]),
         "mpe_destroy": (None, [vp]),
@@ -134,6 +143,11 @@ def lib() -> ctypes.CDLL:
         "mpe_profile_enable": (i32, [vp, i32]),
         "mpe_profile_read": (i32, [vp, vp, vp, i32, i32]),
         "mpe_route_noalloc": (i32, [vp, i32, i32, i32, vp, vp, vp, vp]),
+        "mpe_select_experts": (i32, [vp, vp, i32, i64, i32, vp, vp, vp, vp]),
+        "mpe_expert_importance": (i32, [vp, i32, i64, i32, i32, i32, vp, vp, sz, vp]),
+        "mpe_expert_importance_workspace": (sz, [i32, i32]),
+        "mpe_linear": (i32, [vp, vp]),
+        "mpe_global_status": (i32, [vp, i32]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -216,6 +230,156 @@ def route_noalloc(ids, E: int, perm, offsets, inv):
     T, k = ids.shape
     _check(lib().mpe_route_noalloc(_ptr(ids), T, k, E, _ptr(perm), _ptr(offsets), _ptr(inv),
                                    _stream()))
+
+
+# ---- around the routed experts ------------------------------------------------
+# mpe_select_config and mpe_linear_args as packed bytes
+_SELECT_CONFIG = struct.Struct("=7if")
+_LINEAR_ARGS = struct.Struct("=5Q4q8i")
+_types = None
+
+
+def _type(t, what: str) -> int:
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
+    try:
+        return _types[t.dtype]
+    except KeyError:
+        raise ValueError(f"{what} must be float32, bfloat16 or float16, not {t.dtype}") from None
+
+
+def _matrix(t, what: str, device):
+    """(rows, columns, pitch) of a CUDA matrix whose rows are contiguous."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be a matrix with contiguous rows")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not {device}")
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+def _vector(t, n: int, what: str, device, dtypes):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.dtype not in dtypes:
+        raise ValueError(f"{what} must be a contiguous vector of {n} values of "
+                         f"{' or '.join(str(d) for d in dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not {device}")
+
+
+def _on_device(t, call):
+    """call(stream) -> return code, on t's device and the current stream there."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if t.device.index == torch.cuda.current_device():
+        _check(call(_stream()))
+    else:
+        with torch.cuda.device(t.device):
+            _check(call(_stream()))
+
+
+def select_experts(logits, k: int, *, bias=None, score: int = SCORE_SOFTMAX, n_groups: int = 1,
+                   keep_groups: int | None = None, group_score: int = GROUP_TOP2,
+                   renormalize: bool = True, scale: float = 1.0, ids=None, w=None):
+    """Each token's k experts and weights from router logits [T, E] (float32, bfloat16 or
+    float16, rows contiguous): (ids int32 [T, k], w float32 [T, k]) as ``Context.moe_ffn``
+    takes them. Scores are the softmax or sigmoid of the logits; ``bias`` (float32 [E]) is
+    added for the choice alone; the choice is limited to the ``keep_groups`` best of
+    ``n_groups`` groups of consecutive experts; weights are the chosen scores, divided by
+    their sum with ``renormalize``, times ``scale`` (mpe_select_experts). Current stream."""
+    import torch
+    dev = logits.device
+    T, E, ld = _matrix(logits, "logits", dev)
+    typ = _type(logits, "logits")
+    if bias is not None:
+        _vector(bias, E, "bias", dev, (torch.float32,))
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    elif ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous() or ids.device != dev:
+        raise ValueError(f"ids must be a contiguous int32 [{T}, {k}] on {dev}")
+    if w is None:
+        w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    elif w.shape != (T, k) or w.dtype != torch.float32 or not w.is_contiguous() or w.device != dev:
+        raise ValueError(f"w must be a contiguous float32 [{T}, {k}] on {dev}")
+    cfg = _SELECT_CONFIG.pack(E, k, score, n_groups, n_groups if keep_groups is None else keep_groups,
+                              group_score, 1 if renormalize else 0, scale)
+    f = lib().mpe_select_experts
+    _on_device(logits, lambda st: f(cfg, logits.data_ptr(), typ, max(ld, E) if T <= 1 else ld, T,
+                                    0 if bias is None else bias.data_ptr(), ids.data_ptr(),
+                                    w.data_ptr(), st))
+    return ids, w
+
+
+def expert_importance(logits, *, score: int = SCORE_SOFTMAX, out=None):
+    """float32 [E]: the experts' mean routing scores over a batch of router logits [T, E], the
+    importances p that ``allocate_bits`` and ``Context.repage`` take (mpe_expert_importance).
+    Current stream."""
+    import torch
+    dev = logits.device
+    T, E, ld = _matrix(logits, "logits", dev)
+    typ = _type(logits, "logits")
+    if out is None:
+        out = torch.empty(E, dtype=torch.float32, device=dev)
+    else:
+        _vector(out, E, "out", dev, (torch.float32,))
+    L = lib()
+    need = L.mpe_expert_importance_workspace(T, E)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _on_device(logits, lambda st: L.mpe_expert_importance(
+        logits.data_ptr(), typ, max(ld, E) if T <= 1 else ld, T, E, score, out.data_ptr(),
+        ws.data_ptr() if need else 0, need, st))
+    return out
+
+
+def linear(x, weight, *, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None, out=None,
+           out_dtype=None):
+    """act(x weight^T + bias) + residual for x [M, K] and weight [N, K] (bfloat16 or float16,
+    rows contiguous, 16-byte aligned, pitches multiples of 8); ``gated``: weight [2N, K] holds
+    the gate's rows and then the up projection's, out = act(gate) * up + residual. ``bias`` is
+    of x's type or float32, out (and residual, which may be ``out`` itself) of x's type or
+    float32 (``out_dtype``, default x's) (mpe_linear). Current stream."""
+    import torch
+    dev = x.device
+    M, K, ldx = _matrix(x, "x", dev)
+    R, Kw, ldw = _matrix(weight, "weight", dev)
+    typ = _type(x, "x")
+    if Kw != K or weight.dtype != x.dtype:
+        raise ValueError(f"weight must be {x.dtype} [N, {K}]")
+    if gated and R % 2:
+        raise ValueError("a gated weight has an even number of rows")
+    N = R // 2 if gated else R
+    btyp = 0
+    if bias is not None:
+        _vector(bias, R, "bias", dev, (x.dtype, torch.float32))
+        btyp = _type(bias, "bias")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or (x.dtype if residual is None else residual.dtype),
+                          device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, not {out_dtype}")
+    mo, no, ldo = _matrix(out, "out", dev)
+    if mo != M or no != N:
+        raise ValueError(f"out must be [{M}, {N}]")
+    ldr = 0
+    if residual is not None:
+        mr, nr, ldr = _matrix(residual, "residual", dev)
+        if mr != M or nr != N or residual.dtype != out.dtype:
+            raise ValueError(f"residual must be {out.dtype} [{M}, {N}]")
+    args = _LINEAR_ARGS.pack(x.data_ptr(), weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+                             0 if residual is None else residual.data_ptr(), out.data_ptr(),
+                             ldx, ldw, ldr, ldo, M, N, K, typ, btyp, _type(out, "out"), act,
+                             1 if gated else 0)
+    f = lib().mpe_linear
+    _on_device(x, lambda st: f(args, st))
+    return out
+
+
+def global_status(clear: bool = False) -> int:
+    """The sticky status word of the context-free calls on the current device (synchronises)."""
+    st = ctypes.c_uint32(0)
+    _check(lib().mpe_global_status(ctypes.byref(st), 1 if clear else 0))
+    return st.value
 
 
 class Context:
