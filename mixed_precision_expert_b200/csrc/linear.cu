@@ -1,8 +1,11 @@
 // out = act(x w^T + bias) + residual and its gated form (mpe_linear).
+#include <cuda.h>
+
 #include <cstdio>
 
 #include "internal.h"
 #include "opcheck.h"
+#include "tc.cuh"
 
 namespace mpe {
 namespace {
@@ -10,11 +13,14 @@ namespace {
 // Sticky status of the current device's context-free calls.
 __device__ uint32_t g_status;
 
-struct LinearArgs {
-    const void *x, *w, *bias, *residual;
+// Where a result goes and what is done to it on the way.
+struct Epilogue {
+    const void *bias, *residual;
     void* out;
-    int64_t ldx, ldw, ldr, ldo;
-    int M, N, K, type, bias_type, out_type, act, gated;
+    int64_t ldr, ldo;
+    int M, N;
+    int bias_type, out_type, act;
+    int vec;  // out and residual rows take runs of 4 values at multiples of 4
 };
 
 __device__ __forceinline__ float load_as_float(const void* p, size_t i, int type) {
@@ -26,54 +32,342 @@ __device__ __forceinline__ float load_as_float(const void* p, size_t i, int type
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case MPE_ACT_RELU: return v < 0.0f ? 0.0f : v;
-        case MPE_ACT_SILU: return v / (1.0f + expf(-v));
+        case MPE_ACT_SILU: return __fdividef(v, 1.0f + expf(-v));
         case MPE_ACT_GELU: return 0.5f * v * erfcf(-0.70710678f * v);
-        case MPE_ACT_GELU_TANH: return v / (1.0f + expf(-1.59576912f * (v + 0.044715f * v * v * v)));
+        case MPE_ACT_GELU_TANH: return __fdividef(v, 1.0f + expf(-1.59576912f * (v + 0.044715f * v * v * v)));
         default: return v;
     }
 }
 
-// One 64 x 64 tile of outputs a block, 16 inputs a step, 4 x 4 outputs a thread.
-__global__ void __launch_bounds__(256) k_linear(const LinearArgs a) {
-    __shared__ float xs[16][65], ws[2][16][65];
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-    const int tm = (threadIdx.x / 16) * 4, tn = (threadIdx.x % 16) * 4;
-    float acc[2][4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 16) {
-        for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-            const int r = i / 16, c = i % 16, k = k0 + c;
-            xs[c][r] = m0 + r < a.M && k < a.K ? load_as_float(a.x, (size_t)(m0 + r) * a.ldx + k, a.type) : 0.0f;
-            for (int h = 0; h <= a.gated; ++h)
-                ws[h][c][r] = n0 + r < a.N && k < a.K
-                                  ? load_as_float(a.w, ((size_t)h * a.N + n0 + r) * a.ldw + k, a.type)
-                                  : 0.0f;
-        }
-        __syncthreads();
-        for (int c = 0; c < 16; ++c)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    acc[0][i][j] += xs[c][tm + i] * ws[0][c][tn + j];
-                    if (a.gated) acc[1][i][j] += xs[c][tm + i] * ws[1][c][tn + j];
-                }
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + tm + i, n = n0 + tn + j;
-            if (m >= a.M || n >= a.N) continue;
-            float v = acc[0][i][j], u = acc[1][i][j];
-            if (a.bias) {
-                v += load_as_float(a.bias, n, a.bias_type);
-                if (a.gated) u += load_as_float(a.bias, (size_t)a.N + n, a.bias_type);
+// V values of row m from column n on (V = 2 or 4; n a multiple of V), all of
+// them or those below N.
+template <int V>
+__device__ __forceinline__ void load_run(const Epilogue& e, const void* base, int64_t ld, int m, int n, float (&r)[V]) {
+    const size_t at = (size_t)m * ld + n;
+    if (e.vec && n + V <= e.N) {
+        if (e.out_type == MPE_TYPE_F32) {
+            if constexpr (V == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+                r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(base) + at);
+                r[0] = v.x, r[1] = v.y;
             }
-            v = activate(v, a.act);
-            if (a.gated) v *= u;
-            if (a.residual) v += load_as_float(a.residual, (size_t)m * a.ldr + n, a.out_type);
-            const size_t o = (size_t)m * a.ldo + n;
-            if (a.out_type == MPE_TYPE_F32) static_cast<float*>(a.out)[o] = v;
-            else if (a.out_type == MPE_TYPE_BF16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
-            else static_cast<__half*>(a.out)[o] = __float2half_rn(v);
+        } else {
+            uint32_t h[V / 2];
+            if constexpr (V == 4) {
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+                h[0] = v.x, h[1] = v.y;
+            } else {
+                h[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + at);
+            }
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                float2 f;
+                if (e.out_type == MPE_TYPE_BF16) f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&h[i]));
+                else f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+                r[2 * i] = f.x;
+                r[2 * i + 1] = f.y;
+            }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = n + i < e.N ? load_as_float(base, at + i, e.out_type) : 0.0f;
+    }
+}
+
+// Two values rounded to the output's 16-bit type.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+    uint32_t r;
+    if (type == MPE_TYPE_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        memcpy(&r, &v, 4);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        memcpy(&r, &v, 4);
+    }
+    return r;
+}
+
+template <int V>
+__device__ __forceinline__ void store_run(const Epilogue& e, int m, int n, const float (&r)[V]) {
+    const size_t at = (size_t)m * e.ldo + n;
+    if (e.vec && n + V <= e.N) {
+        if (e.out_type == MPE_TYPE_F32) {
+            float* p = static_cast<float*>(e.out) + at;
+            if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
+            else *reinterpret_cast<float2*>(p) = make_float2(r[0], r[1]);
+        } else {
+            uint16_t* p = static_cast<uint16_t*>(e.out) + at;
+            if constexpr (V == 4)
+                *reinterpret_cast<uint2*>(p) = make_uint2(pack2(r[0], r[1], e.out_type), pack2(r[2], r[3], e.out_type));
+            else *reinterpret_cast<uint32_t*>(p) = pack2(r[0], r[1], e.out_type);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (n + i >= e.N) break;
+            if (e.out_type == MPE_TYPE_F32) static_cast<float*>(e.out)[at + i] = r[i];
+            else if (e.out_type == MPE_TYPE_BF16) static_cast<__nv_bfloat16*>(e.out)[at + i] = __float2bfloat16_rn(r[i]);
+            else static_cast<__half*>(e.out)[at + i] = __float2half_rn(r[i]);
+        }
+    }
+}
+
+// out[m, n .. n + V - 1] from the product's sums v (and the up projection's, u).
+template <int V, bool GATED>
+__device__ __forceinline__ void finish(const Epilogue& e, int m, int n, float (&v)[V], const float (&u)[V]) {
+    if (n >= e.N) return;
+    float r[V];
+    if (e.residual) load_run<V>(e, e.residual, e.ldr, m, n, r);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float up = u[i];
+        if (e.bias && n + i < e.N) {
+            v[i] += load_as_float(e.bias, n + i, e.bias_type);
+            if (GATED) up += load_as_float(e.bias, (size_t)e.N + n + i, e.bias_type);
+        }
+        v[i] = activate(v[i], e.act);
+        if (GATED) v[i] *= up;
+        if (e.residual) v[i] += r[i];
+    }
+    store_run<V>(e, m, n, v);
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the weights stream once, their rows are the MMA's M
+// ---------------------------------------------------------------------------
+// One CTA multiplies 128 rows of w (gated: 64 of the gate's and the same 64 of
+// the up projection's) with NT tokens over a share of K; the CTAs of a cluster
+// share K, leave their sums in their own shared memory, and each adds up and
+// finishes every S-th token of the tile in the order of the ranks, so that the
+// result does not depend on timing and no workspace is needed.
+//   warp 0   loads: per step of 64 inputs one box of w (gated: two) and one of x
+//   warp 1   MMAs, M = 128, N = NT
+//   all      tensor memory -> shared memory, sum over the cluster, epilogue
+constexpr int kKStep = 64;
+constexpr int kRows = 128;
+
+template <int NT>
+struct Narrow {
+    static constexpr int kStageBytes = (kRows + NT) * 128;
+    static constexpr int kStages = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : NT <= 128 ? 3 : 4;
+    static constexpr int kPartBytes = NT * kRows * 4;
+    static constexpr int kRing = kStages * kStageBytes > kPartBytes ? kStages * kStageBytes : kPartBytes;
+    static constexpr int kSmem = 1024 + kRing + 256;
+    static constexpr int kCols = NT < 32 ? 32 : NT;
+};
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(128)
+k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Epilogue e,
+         const int nk, const uint32_t idesc) {
+    using C = Narrow<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kRing);
+    uint64_t* empty = full + C::kStages;
+    uint64_t* done = empty + C::kStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t S;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+    const uint32_t rank = tc::cluster_rank();
+    const int n0 = (int)(blockIdx.x / S) * (GATED ? kRows / 2 : kRows);
+    const int m0 = (int)blockIdx.y * NT;
+    const int k_first = (int)((int64_t)nk * rank / S), k_last = (int)((int64_t)nk * (rank + 1) / S);
+
+    if (threadIdx.x == 0) {
+        tc::prefetch_map(&map_w);
+        tc::prefetch_map(&map_x);
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 0;
+            for (int k = k_first; k < k_last; ++k) {
+                if (k - k_first >= C::kStages && !mbar_wait_bounded(&empty[s], phase ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = smem_u32(ring + s * C::kStageBytes);
+                mbar_arrive_expect_tx(&full[s], (uint32_t)C::kStageBytes);
+                if (GATED) {
+                    tc::load_box(dst, &map_w, kKStep * k, n0, &full[s]);
+                    tc::load_box(dst + kRows / 2 * 128, &map_w, kKStep * k, e.N + n0, &full[s]);
+                } else {
+                    tc::load_box(dst, &map_w, kKStep * k, n0, &full[s]);
+                }
+                tc::load_box(dst + kRows * 128, &map_x, kKStep * k, m0, &full[s]);
+                if (++s == C::kStages) s = 0, phase ^= 1u;
+            }
+            // on a failed wait, time for copies in flight to land
+            if (!ok)
+                for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000ull;) {
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // tensor memory is taken after the wait for earlier kernels, and the next
+        // kernel may start only when this one has it: neither can block the other
+        tc::tmem_alloc(tmem_slot, C::kCols);
+        __syncwarp();
+        if (lane == 0) {
+            griddep_launch_dependents();
+            const uint32_t d = *tmem_slot;
+            const uint64_t desc = tc::smem_desc(smem_u32(ring));
+            int s = 0;
+            uint32_t phase = 0;
+            for (int k = k_first; k < k_last; ++k) {
+                if (!mbar_wait_spin(&full[s], phase)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (kRows * 128 >> 4);
+#pragma unroll
+                for (int i = 0; i < kKStep / 16; ++i)
+                    tc::mma(d, da + 2 * i, db + 2 * i, idesc, k > k_first || i > 0);
+                tc::commit(&empty[s]);
+                if (++s == C::kStages) s = 0, phase ^= 1u;
+            }
+            tc::commit(done);
+        }
+        __syncwarp();
+    }
+    ok &= mbar_wait_bounded(done, 0);
+    tc::fence_after();
+    ok = __syncthreads_and(ok);
+    if (!ok && threadIdx.x == 0) set_status(&g_status, MPE_STATUS_WAIT_TIMEOUT);
+    // sums of this share of K, token-major: part[token][row]
+    float* part = reinterpret_cast<float*>(ring);
+    const uint32_t tbase = *tmem_slot;
+    const int mt = min(NT, e.M - m0);
+    if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < mt; c += 16) {
+            uint32_t r[16];
+            tc::tmem_load16(tbase + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, r);
+            tc::tmem_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(c + i) * kRows + threadIdx.x] = __uint_as_float(r[i]);
+        }
+    }
+    tc::fence_before();
+    if (S > 1) tc::cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_free(tbase, C::kCols);
+    }
+    // every S-th token, one warp each; a lane has 4 outputs (gated: 2)
+    constexpr int V = GATED ? 2 : 4;
+    const uint32_t mine = smem_u32(part);
+    for (int t = (int)rank + (int)S * warp; t < mt; t += 4 * (int)S) {
+        float v[V], u[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = u[i] = 0.0f;
+        const uint32_t at = mine + (uint32_t)(t * kRows + V * lane) * 4;
+#pragma unroll 8
+        for (uint32_t s = 0; s < S; ++s) {
+            const uint32_t p = tc::peer_addr(at, s);
+            if constexpr (GATED) {
+                const float2 g = tc::peer_load2(p), w = tc::peer_load2(p + kRows / 2 * 4);
+                v[0] += g.x, v[1] += g.y, u[0] += w.x, u[1] += w.y;
+            } else {
+                const float4 g = tc::peer_load4(p);
+                v[0] += g.x, v[1] += g.y, v[2] += g.z, v[3] += g.w;
+            }
+        }
+        finish<V, GATED>(e, m0 + t, n0 + V * lane, v, u);
+    }
+    if (S > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+typedef CUresult (*TensorMapEncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                         const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                         CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                         CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once through the runtime.
+TensorMapEncodeTiled encoder() {
+    static const TensorMapEncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<TensorMapEncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// [rows x K] 16-bit values with pitch ld, read as boxes of box_rows x 64.
+bool encode(CUtensorMap* map, const void* base, int type, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+    TensorMapEncodeTiled enc = encoder();
+    if (!enc) return false;
+    if (rows == 1) ld = (K + 7) / 8 * 8;  // a single row's pitch is not used, but has to be valid
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kKStep, (cuuint32_t)box_rows};
+    const cuuint32_t ones[2] = {1, 1};
+    return enc(map, type == MPE_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+               const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, bool GATED>
+cudaError_t launch_narrow(const mpe_linear_args& p, const Epilogue& e, int split, cudaStream_t st) {
+    using C = Narrow<NT>;
+    alignas(64) CUtensorMap mw, mx;
+    const int64_t wrows = GATED ? 2 * (int64_t)p.N : p.N;
+    if (!encode(&mw, p.w, p.type, wrows, p.K, p.ldw, GATED ? kRows / 2 : kRows) ||
+        !encode(&mx, p.x, p.type, p.M, p.K, p.ldx, NT))
+        return cudaErrorInvalidValue;
+    cudaError_t err = cudaFuncSetAttribute(k_narrow<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    const int per = GATED ? kRows / 2 : kRows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.N + per - 1) / per * split), (unsigned)((p.M + NT - 1) / NT));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_narrow<NT, GATED>, mw, mx, e, (p.K + kKStep - 1) / kKStep,
+                              tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
+}
+
+template <bool GATED>
+cudaError_t launch_narrow_for(const mpe_linear_args& p, const Epilogue& e, cudaStream_t st, int sms) {
+    const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+    const int per = GATED ? kRows / 2 : kRows;
+    const int64_t tiles = (int64_t)((p.N + per - 1) / per) * ((p.M + nt - 1) / nt);
+    const int nk = (p.K + kKStep - 1) / kKStep;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2 * sms && nk >= 4 * split) split *= 2;
+    switch (nt) {
+        case 16: return launch_narrow<16, GATED>(p, e, split, st);
+        case 32: return launch_narrow<32, GATED>(p, e, split, st);
+        case 64: return launch_narrow<64, GATED>(p, e, split, st);
+        default: return launch_narrow<128, GATED>(p, e, split, st);
+    }
 }
 
 // rows of `cols` values of sz bytes, ld values apart, as a set of bytes
@@ -143,12 +437,18 @@ extern "C" int mpe_linear(const mpe_linear_args* p, void* stream) {
     if (p->residual && !(p->residual == p->out && (p->M == 1 || p->ldr == p->ldo)) &&
         overlap(out, Block(p->residual, p->M, p->N, p->ldr, osz)))
         return report_global_errorf(MPE_ERR_INVALID, "%s: out overlaps residual without being it", who);
-    LinearArgs a{p->x,   p->w,   p->bias, p->residual, p->out,       p->ldx,      p->ldw, p->ldr,      p->ldo,
-                 p->M,   p->N,   p->K,    p->type,     p->bias_type, p->out_type, p->act, p->gated != 0};
+    // runs of 4 outputs: rows start at multiples of 4 values
+    auto runs = [&](const void* base, int64_t ld) { return aligned(base, 4 * osz) && (p->M == 1 || ld % 4 == 0); };
+    const int vec = runs(p->out, p->ldo) && (!p->residual || runs(p->residual, p->ldr));
+    const Epilogue e{p->bias, p->residual, p->out, p->ldr, p->ldo, p->M, p->N, p->bias_type, p->out_type, p->act, vec};
+    const int sms = current_sm_count();
+    if (sms <= 0) return report_global_errorf(MPE_ERR_CUDA, "%s: no current device", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    k_linear<<<dim3((p->N + 63) / 64, (p->M + 63) / 64), 256, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return report_global_errorf(MPE_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    const cudaError_t err = p->gated ? launch_narrow_for<true>(*p, e, st, sms) : launch_narrow_for<false>(*p, e, st, sms);
+    if (err != cudaSuccess) {
+        cudaGetLastError();  // reported here, not left for the next call
+        return report_global_errorf(MPE_ERR_CUDA, "%s: %s", who, cudaGetErrorString(err));
+    }
     return MPE_OK;
 }
 
