@@ -237,46 +237,67 @@ def route_noalloc(ids, E: int, perm, offsets, inv):
 _SELECT_CONFIG = struct.Struct("=7if")
 _LINEAR_ARGS = struct.Struct("=5Q4q8i")
 _types = None
+_cuda = None  # torch's (current device, current stream's handle) queries
+
+
+def _lookup():
+    """torch's types by MPE_TYPE_* and its device and stream queries (the handles that
+    torch.cuda.current_device() and current_stream() wrap, at a twentieth of their time)."""
+    global _types, _cuda
+    import torch
+    _types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
+    torch.cuda.current_device()  # initialises CUDA
+    _cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+
+
+def _call(f, dev: int, *args):
+    """f(*args, stream) on device `dev` and its current stream."""
+    device, stream = _cuda
+    if dev == device():
+        rc = f(*args, stream(dev))
+    else:
+        import torch
+        with torch.cuda.device(dev):
+            rc = f(*args, stream(dev))
+    if rc != MPE_OK:
+        _check(rc)
+
+
+def _device(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if _cuda is None:
+        _lookup()
+    return dev
 
 
 def _type(t, what: str) -> int:
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
-    try:
-        return _types[t.dtype]
-    except KeyError:
-        raise ValueError(f"{what} must be float32, bfloat16 or float16, not {t.dtype}") from None
+    typ = _types.get(t.dtype)
+    if typ is None:
+        raise ValueError(f"{what} must be float32, bfloat16 or float16, not {t.dtype}")
+    return typ
 
 
-def _matrix(t, what: str, device):
-    """(rows, columns, pitch) of a CUDA matrix whose rows are contiguous."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{what} must be a matrix with contiguous rows")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not {device}")
-    return t.shape[0], t.shape[1], t.stride(0)
+def _matrix(t, what: str, dev: int):
+    """((rows, columns), pitch) of a matrix with contiguous rows on device dev."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be a matrix")
+    pitch, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, not on CUDA device {dev}")
+    return shape, pitch
 
 
-def _vector(t, n: int, what: str, device, dtypes):
+def _vector(t, n: int, what: str, dev: int, dtypes):
     if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.dtype not in dtypes:
         raise ValueError(f"{what} must be a contiguous vector of {n} values of "
                          f"{' or '.join(str(d) for d in dtypes)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not {device}")
-
-
-def _on_device(t, call):
-    """call(stream) -> return code, on t's device and the current stream there."""
-    import torch
-    if not t.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    if t.device.index == torch.cuda.current_device():
-        _check(call(_stream()))
-    else:
-        with torch.cuda.device(t.device):
-            _check(call(_stream()))
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, not on CUDA device {dev}")
 
 
 def select_experts(logits, k: int, *, bias=None, score: int = SCORE_SOFTMAX, n_groups: int = 1,
@@ -289,25 +310,23 @@ def select_experts(logits, k: int, *, bias=None, score: int = SCORE_SOFTMAX, n_g
     ``n_groups`` groups of consecutive experts; weights are the chosen scores, divided by
     their sum with ``renormalize``, times ``scale`` (mpe_select_experts). Current stream."""
     import torch
-    dev = logits.device
-    T, E, ld = _matrix(logits, "logits", dev)
+    dev = _device(logits)
+    (T, E), ld = _matrix(logits, "logits", dev)
     typ = _type(logits, "logits")
     if bias is not None:
         _vector(bias, E, "bias", dev, (torch.float32,))
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    elif ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous() or ids.device != dev:
-        raise ValueError(f"ids must be a contiguous int32 [{T}, {k}] on {dev}")
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    elif ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous() or ids.get_device() != dev:
+        raise ValueError(f"ids must be a contiguous int32 [{T}, {k}] on CUDA device {dev}")
     if w is None:
-        w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    elif w.shape != (T, k) or w.dtype != torch.float32 or not w.is_contiguous() or w.device != dev:
-        raise ValueError(f"w must be a contiguous float32 [{T}, {k}] on {dev}")
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    elif w.shape != (T, k) or w.dtype != torch.float32 or not w.is_contiguous() or w.get_device() != dev:
+        raise ValueError(f"w must be a contiguous float32 [{T}, {k}] on CUDA device {dev}")
     cfg = _SELECT_CONFIG.pack(E, k, score, n_groups, n_groups if keep_groups is None else keep_groups,
                               group_score, 1 if renormalize else 0, scale)
-    f = lib().mpe_select_experts
-    _on_device(logits, lambda st: f(cfg, logits.data_ptr(), typ, max(ld, E) if T <= 1 else ld, T,
-                                    0 if bias is None else bias.data_ptr(), ids.data_ptr(),
-                                    w.data_ptr(), st))
+    _call(lib().mpe_select_experts, dev, cfg, logits.data_ptr(), typ, ld if T > 1 else max(ld, E), T,
+          0 if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr())
     return ids, w
 
 
@@ -316,19 +335,18 @@ def expert_importance(logits, *, score: int = SCORE_SOFTMAX, out=None):
     importances p that ``allocate_bits`` and ``Context.repage`` take (mpe_expert_importance).
     Current stream."""
     import torch
-    dev = logits.device
-    T, E, ld = _matrix(logits, "logits", dev)
+    dev = _device(logits)
+    (T, E), ld = _matrix(logits, "logits", dev)
     typ = _type(logits, "logits")
     if out is None:
-        out = torch.empty(E, dtype=torch.float32, device=dev)
+        out = torch.empty(E, dtype=torch.float32, device=logits.device)
     else:
         _vector(out, E, "out", dev, (torch.float32,))
     L = lib()
     need = L.mpe_expert_importance_workspace(T, E)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _on_device(logits, lambda st: L.mpe_expert_importance(
-        logits.data_ptr(), typ, max(ld, E) if T <= 1 else ld, T, E, score, out.data_ptr(),
-        ws.data_ptr() if need else 0, need, st))
+    ws = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
+    _call(L.mpe_expert_importance, dev, logits.data_ptr(), typ, ld if T > 1 else max(ld, E), T, E, score,
+          out.data_ptr(), ws.data_ptr() if need else 0, need)
     return out
 
 
@@ -338,40 +356,38 @@ def linear(x, weight, *, bias=None, act: int = ACT_NONE, gated: bool = False, re
     rows contiguous, 16-byte aligned, pitches multiples of 8); ``gated``: weight [2N, K] holds
     the gate's rows and then the up projection's, out = act(gate) * up + residual. ``bias`` is
     of x's type or float32, out (and residual, which may be ``out`` itself) of x's type or
-    float32 (``out_dtype``, default x's) (mpe_linear). Current stream."""
-    import torch
-    dev = x.device
-    M, K, ldx = _matrix(x, "x", dev)
-    R, Kw, ldw = _matrix(weight, "weight", dev)
+    float32 (``out_dtype``, default the residual's or x's) (mpe_linear). Current stream."""
+    dev = _device(x)
+    (M, K), ldx = _matrix(x, "x", dev)
+    (R, Kw), ldw = _matrix(weight, "weight", dev)
     typ = _type(x, "x")
     if Kw != K or weight.dtype != x.dtype:
         raise ValueError(f"weight must be {x.dtype} [N, {K}]")
     if gated and R % 2:
         raise ValueError("a gated weight has an even number of rows")
     N = R // 2 if gated else R
-    btyp = 0
+    bptr = btyp = rptr = ldr = 0
     if bias is not None:
+        import torch
         _vector(bias, R, "bias", dev, (x.dtype, torch.float32))
-        btyp = _type(bias, "bias")
+        bptr, btyp = bias.data_ptr(), _type(bias, "bias")
     if out is None:
+        import torch
         out = torch.empty((M, N), dtype=out_dtype or (x.dtype if residual is None else residual.dtype),
-                          device=dev)
+                          device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
-    mo, no, ldo = _matrix(out, "out", dev)
-    if mo != M or no != N:
+    shape, ldo = _matrix(out, "out", dev)
+    if shape != (M, N):
         raise ValueError(f"out must be [{M}, {N}]")
-    ldr = 0
     if residual is not None:
-        mr, nr, ldr = _matrix(residual, "residual", dev)
-        if mr != M or nr != N or residual.dtype != out.dtype:
+        shape, ldr = _matrix(residual, "residual", dev)
+        if shape != (M, N) or residual.dtype != out.dtype:
             raise ValueError(f"residual must be {out.dtype} [{M}, {N}]")
-    args = _LINEAR_ARGS.pack(x.data_ptr(), weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
-                             0 if residual is None else residual.data_ptr(), out.data_ptr(),
-                             ldx, ldw, ldr, ldo, M, N, K, typ, btyp, _type(out, "out"), act,
-                             1 if gated else 0)
-    f = lib().mpe_linear
-    _on_device(x, lambda st: f(args, st))
+        rptr = residual.data_ptr()
+    args = _LINEAR_ARGS.pack(x.data_ptr(), weight.data_ptr(), bptr, rptr, out.data_ptr(), ldx, ldw, ldr, ldo,
+                             M, N, K, typ, btyp, _type(out, "out"), act, 1 if gated else 0)
+    _call(lib().mpe_linear, dev, args)
     return out
 
 

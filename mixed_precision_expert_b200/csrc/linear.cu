@@ -2,6 +2,8 @@
 #include <cuda.h>
 
 #include <cstdio>
+#include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "opcheck.h"
@@ -294,6 +296,301 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
     if (S > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: tiles of 256 tokens by BN rows of w, a pair of CTAs each
+// ---------------------------------------------------------------------------
+// The tokens are the MMA's M (128 in each CTA), BN rows of w its N: each CTA
+// loads its tokens and half of the rows of w (gated: rank 0 the gate's, rank 1
+// the up projection's rows of the same BN / 2 outputs, so that a thread finds
+// both in its own accumulator), and rank 0 issues the MMAs for both. A pair
+// takes tiles in turn; two accumulators let the MMAs of a tile run while the
+// one before is finished.
+//   warp 0     loads into a ring of K-steps of 64
+//   warp 1     MMAs (rank 0)
+//   warps 4-7  epilogue, 32 tokens each: a thread has a token's outputs, which
+//              go through 4 KB of shared memory a warp, so that global memory is
+//              read and written in runs of whole rows
+template <int BN>
+struct Wide {
+    static constexpr int kStageBytes = 128 * 128 + BN / 2 * 128;
+    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int kStaging = 4 * 4096;
+    static constexpr int kSmem = 1024 + kRing + kStaging + 4 * BN * 4 + 256;
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+    static constexpr int kCols = 2 * BN;
+    static_assert(kCols <= 512, "tensor memory");
+};
+constexpr int kWideThreads = 256;
+constexpr int kTileM = 256;
+
+struct Tiles {
+    int m, n;  // tiles of tokens, of outputs
+};
+
+// Tile t of the walk: bands of 8 token tiles, in a band one column of tiles after
+// the other, so that the tiles in flight share rows of x and of w in L2.
+__device__ __forceinline__ void tile_at(const Tiles& g, int64_t t, int& m, int& n) {
+    const int64_t band = t / ((int64_t)8 * g.n);
+    const int64_t in = t - band * 8 * g.n;
+    const int first = (int)band * 8, rows = min(8, g.m - first);
+    n = (int)(in / rows);
+    m = first + (int)(in - (int64_t)n * rows);
+}
+
+// A warp's 32 rows of 128 bytes: 16-byte piece j of row r lies at j ^ (r & 7).
+__device__ __forceinline__ uint8_t* staged(uint8_t* base, int r, int j) { return base + r * 128 + ((j ^ (r & 7)) << 4); }
+
+// Between the staging rows and global rows m .. m + 31, columns n .. (128 bytes'
+// worth): 16-byte pieces where `runs`, single values otherwise.
+template <int SZ, bool STORE>
+__device__ __forceinline__ void move_rows(uint8_t* stage, void* base, int64_t ld, int m, int n, int M, int N, bool runs,
+                                          int lane) {
+    using V = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
+    constexpr int kPer = 16 / SZ, kCols = 128 / SZ;
+    V* g = static_cast<V*>(base);
+    if (runs) {
+        const int j = lane & 7, c = n + j * kPer;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            if (m + r >= M || c >= N) continue;
+            V* p = g + (size_t)(m + r) * ld + c;
+            uint8_t* s = staged(stage, r, j);
+            if (c + kPer <= N) {
+                if (STORE) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(s);
+                else *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(p);
+            } else {
+                for (int q = 0; c + q < N; ++q) {
+                    if (STORE) p[q] = reinterpret_cast<const V*>(s)[q];
+                    else reinterpret_cast<V*>(s)[q] = p[q];
+                }
+            }
+        }
+    } else {
+        for (int r = 0; r < 32 && m + r < M; ++r)
+#pragma unroll
+            for (int c = lane; c < kCols; c += 32) {
+                if (n + c >= N) continue;
+                V* p = g + (size_t)(m + r) * ld + n + c;
+                V* s = reinterpret_cast<V*>(staged(stage, r, c / kPer)) + c % kPer;
+                if (STORE) *p = *s;
+                else *s = *p;
+            }
+    }
+}
+
+template <int BN, bool GATED, int SZ>
+__global__ void __launch_bounds__(kWideThreads, 1)
+k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Epilogue e,
+       const Tiles grid, const int nk, const uint32_t idesc) {
+    using C = Wide<BN>;
+    constexpr int kOut = GATED ? BN / 2 : BN;  // outputs of a tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* staging = ring + C::kRing;
+    float* s_bias = reinterpret_cast<float*>(staging + C::kStaging);  // [epilogue warps][BN]
+    uint64_t* full = reinterpret_cast<uint64_t*>(s_bias + 4 * BN);    // rank 0: both CTAs' boxes of a stage
+    uint64_t* empty = full + C::kStages;                              // each CTA: its stage was multiplied
+    uint64_t* acc_full = empty + C::kStages;                          // each CTA: [2] accumulator complete
+    uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by the 8 epilogue warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_rank();
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int64_t tiles = (int64_t)grid.m * grid.n;
+
+    if (threadIdx.x == 0) {
+        tc::prefetch_map(&map_x);
+        tc::prefetch_map(&map_w);
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 8);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    if (warp == 1) tc::tmem_alloc_pair(tmem_slot, C::kCols);  // after the wait, as in k_narrow
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    const uint32_t tbase = *tmem_slot;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 0;
+            bool again = false;  // the ring has been filled once
+            for (int64_t t = pair; t < tiles && ok; t += pairs) {
+                int m, n;
+                tile_at(grid, t, m, n);
+                const int x_row = m * kTileM + rank * 128;
+                const int w_row = GATED ? n * kOut + (rank ? e.N : 0) : n * kOut + rank * (BN / 2);
+                for (int k = 0; k < nk; ++k) {
+                    if (again && !mbar_wait_bounded(&empty[s], phase ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = smem_u32(ring + s * C::kStageBytes);
+                    const uint32_t bar = tc::peer_addr(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * C::kStageBytes);
+                    tc::load_box_pair(dst, &map_x, kKStep * k, x_row, bar);
+                    tc::load_box_pair(dst + 128 * 128, &map_w, kKStep * k, w_row, bar);
+                    if (++s == C::kStages) s = 0, phase ^= 1u, again = true;
+                }
+            }
+            // every stage that was filled has been multiplied: nothing arrives here any more
+            for (int i = 0; i < C::kStages && ok; ++i) {
+                if (!again && i >= s) break;
+                const bool earlier = i >= s;  // filled in the round before this one
+                ok = mbar_wait_bounded(&empty[i], earlier ? phase ^ 1u : phase);
+            }
+            if (!ok)
+                for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000ull;) {
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            const uint64_t desc = tc::smem_desc(smem_u32(ring));
+            int s = 0, b = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            int64_t done = 0;
+            for (int64_t t = pair; t < tiles && ok; t += pairs, ++done) {
+                if (done >= 2 && !mbar_wait_bounded(&acc_empty[b], acc_phase ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t d = tbase + (uint32_t)(b * BN);
+                for (int k = 0; k < nk; ++k) {
+                    if (!mbar_wait_spin(&full[s], phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (128 * 128 >> 4);
+#pragma unroll
+                    for (int i = 0; i < kKStep / 16; ++i)
+                        tc::mma_pair(d, da + 2 * i, db + 2 * i, idesc, k > 0 || i > 0);
+                    tc::commit_pair(&empty[s]);
+                    if (++s == C::kStages) s = 0, phase ^= 1u;
+                }
+                tc::commit_pair(&acc_full[b]);
+                if (++b == 2) b = 0, acc_phase ^= 1u;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int q = warp - 4;
+        uint8_t* stage = staging + q * 4096;
+        float* bias = s_bias + q * BN;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        constexpr int kChunk = 128 / SZ;  // outputs in a staging row
+        int b = 0;
+        uint32_t phase = 0;
+        for (int64_t t = pair; t < tiles && ok; t += pairs) {
+            int mt, nt;
+            tile_at(grid, t, mt, nt);
+            const int m = mt * kTileM + rank * 128 + q * 32, n0 = nt * kOut;
+            if (e.bias) {
+                // [0, kOut): of the outputs (the gate's); [kOut, 2 kOut): the up projection's
+                for (int i = lane; i < BN; i += 32) {
+                    const int n = n0 + i % kOut;
+                    bias[i] = n < e.N ? load_as_float(e.bias, (size_t)(i / kOut) * e.N + n, e.bias_type) : 0.0f;
+                }
+                __syncwarp();
+            }
+            if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            tc::fence_after();
+            const uint32_t acc = tbase + lanes + (uint32_t)(b * BN);
+#pragma unroll 1
+            for (int c = 0; c < kOut && ok; c += kChunk) {
+                if (n0 + c >= e.N || m >= e.M) break;
+                if (e.residual) {
+                    move_rows<SZ, false>(stage, const_cast<void*>(e.residual), e.ldr, m, n0 + c, e.M, e.N, e.vec, lane);
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int h = 0; h < kChunk; h += 16) {
+                    uint32_t v[16], u[16];
+                    tc::tmem_load16(acc + (uint32_t)(c + h), v);
+                    if (GATED) tc::tmem_load16(acc + (uint32_t)(kOut + c + h), u);
+                    tc::tmem_wait();
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        f[i] = __uint_as_float(v[i]);
+                        if (e.bias) f[i] += bias[c + h + i];
+                        f[i] = activate(f[i], e.act);
+                        if (GATED) f[i] *= __uint_as_float(u[i]) + (e.bias ? bias[kOut + c + h + i] : 0.0f);
+                    }
+#pragma unroll
+                    for (int j = 0; j < SZ; ++j) {  // 16 SZ bytes in pieces of 16
+                        uint4* p = reinterpret_cast<uint4*>(staged(stage, lane, h * SZ / 16 + j));
+                        constexpr int kPer = 16 / SZ;
+                        uint32_t w[4];
+                        if (e.residual) {
+                            const uint4 old = *p;
+                            w[0] = old.x, w[1] = old.y, w[2] = old.z, w[3] = old.w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (SZ == 4) {
+                                float r = f[j * kPer + i];
+                                if (e.residual) r += __uint_as_float(w[i]);
+                                w[i] = __float_as_uint(r);
+                            } else {
+                                float lo = f[j * kPer + 2 * i], hi = f[j * kPer + 2 * i + 1];
+                                if (e.residual) {
+                                    float2 o;
+                                    if (e.out_type == MPE_TYPE_BF16) {
+                                        __nv_bfloat162 x2;
+                                        memcpy(&x2, &w[i], 4);
+                                        o = __bfloat1622float2(x2);
+                                    } else {
+                                        __half2 x2;
+                                        memcpy(&x2, &w[i], 4);
+                                        o = __half22float2(x2);
+                                    }
+                                    lo += o.x;
+                                    hi += o.y;
+                                }
+                                w[i] = pack2(lo, hi, e.out_type);
+                            }
+                        }
+                        *p = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                __syncwarp();
+                move_rows<SZ, true>(stage, e.out, e.ldo, m, n0 + c, e.M, e.N, e.vec, lane);
+                __syncwarp();
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::peer_arrive(tc::peer_addr(smem_u32(&acc_empty[b]), 0));
+            if (++b == 2) b = 0, phase ^= 1u;
+        }
+    }
+    if (!ok && lane == 0) set_status(&g_status, MPE_STATUS_WAIT_TIMEOUT);
+    tc::fence_before();
+    __syncwarp();
+    tc::cluster_sync();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_free_pair(tbase, C::kCols);
+    }
+}
+
 typedef CUresult (*TensorMapEncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                          const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                                          CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -370,6 +667,41 @@ cudaError_t launch_narrow_for(const mpe_linear_args& p, const Epilogue& e, cudaS
     }
 }
 
+template <int BN, bool GATED, int SZ>
+cudaError_t launch_wide(const mpe_linear_args& p, const Epilogue& e, int sms, cudaStream_t st) {
+    using C = Wide<BN>;
+    alignas(64) CUtensorMap mx, mw;
+    const int64_t wrows = GATED ? 2 * (int64_t)p.N : p.N;
+    if (!encode(&mx, p.x, p.type, p.M, p.K, p.ldx, 128) || !encode(&mw, p.w, p.type, wrows, p.K, p.ldw, BN / 2))
+        return cudaErrorInvalidValue;
+    cudaError_t err = cudaFuncSetAttribute(k_wide<BN, GATED, SZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    constexpr int kOut = GATED ? BN / 2 : BN;
+    const Tiles g{(p.M + kTileM - 1) / kTileM, (p.N + kOut - 1) / kOut};
+    const int64_t tiles = (int64_t)g.m * g.n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)(tiles < sms / 2 ? tiles : sms / 2));
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_wide<BN, GATED, SZ>, mx, mw, e, g, (p.K + kKStep - 1) / kKStep,
+                              tc::instr_desc(kTileM, BN, p.type == MPE_TYPE_BF16));
+}
+
+template <int BN>
+cudaError_t launch_wide_for(const mpe_linear_args& p, const Epilogue& e, int sms, cudaStream_t st) {
+    if (p.out_type == MPE_TYPE_F32)
+        return p.gated ? launch_wide<BN, true, 4>(p, e, sms, st) : launch_wide<BN, false, 4>(p, e, sms, st);
+    return p.gated ? launch_wide<BN, true, 2>(p, e, sms, st) : launch_wide<BN, false, 2>(p, e, sms, st);
+}
+
 // rows of `cols` values of sz bytes, ld values apart, as a set of bytes
 struct Block {
     uintptr_t base;
@@ -437,14 +769,18 @@ extern "C" int mpe_linear(const mpe_linear_args* p, void* stream) {
     if (p->residual && !(p->residual == p->out && (p->M == 1 || p->ldr == p->ldo)) &&
         overlap(out, Block(p->residual, p->M, p->N, p->ldr, osz)))
         return report_global_errorf(MPE_ERR_INVALID, "%s: out overlaps residual without being it", who);
-    // runs of 4 outputs: rows start at multiples of 4 values
-    auto runs = [&](const void* base, int64_t ld) { return aligned(base, 4 * osz) && (p->M == 1 || ld % 4 == 0); };
+    // many tokens: from two tiles of 128 on
+    const bool wide = p->M > 128;
+    // rows start where runs of 16 bytes (narrow: of 4 values) do
+    const int run = wide ? 16 : 4 * osz;
+    auto runs = [&](const void* base, int64_t ld) { return aligned(base, run) && (p->M == 1 || ld * osz % run == 0); };
     const int vec = runs(p->out, p->ldo) && (!p->residual || runs(p->residual, p->ldr));
     const Epilogue e{p->bias, p->residual, p->out, p->ldr, p->ldo, p->M, p->N, p->bias_type, p->out_type, p->act, vec};
     const int sms = current_sm_count();
     if (sms <= 0) return report_global_errorf(MPE_ERR_CUDA, "%s: no current device", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t err = p->gated ? launch_narrow_for<true>(*p, e, st, sms) : launch_narrow_for<false>(*p, e, st, sms);
+    const cudaError_t err = wide       ? launch_wide_for<256>(*p, e, sms, st)
+                            : p->gated ? launch_narrow_for<true>(*p, e, st, sms) : launch_narrow_for<false>(*p, e, st, sms);
     if (err != cudaSuccess) {
         cudaGetLastError();  // reported here, not left for the next call
         return report_global_errorf(MPE_ERR_CUDA, "%s: %s", who, cudaGetErrorString(err));
