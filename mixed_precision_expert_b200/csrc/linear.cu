@@ -31,50 +31,54 @@ __device__ __forceinline__ float load_as_float(const void* p, size_t i, int type
     return __half2float(static_cast<const __half*>(p)[i]);
 }
 
-__device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {
-        case MPE_ACT_RELU: return v < 0.0f ? 0.0f : v;
-        case MPE_ACT_SILU: return __fdividef(v, 1.0f + expf(-v));
-        case MPE_ACT_GELU: return 0.5f * v * erfcf(-0.70710678f * v);
-        case MPE_ACT_GELU_TANH: return __fdividef(v, 1.0f + expf(-1.59576912f * (v + 0.044715f * v * v * v)));
-        default: return v;
+// The activation of V values: the choice is outside the loop, so that the code of
+// each stands here once a call.
+template <int V>
+__device__ __forceinline__ void activate(float (&v)[V], int act) {
+    if (act == MPE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = __fdividef(v[i], 1.0f + expf(-v[i]));
+    } else if (act == MPE_ACT_GELU_TANH) {
+        // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = __fdividef(v[i], 1.0f + expf(-1.59576912f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+    } else if (act == MPE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678f * v[i]);
+    } else if (act == MPE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
     }
 }
 
-// V values of row m from column n on (V = 2 or 4; n a multiple of V), all of
-// them or those below N.
-template <int V>
-__device__ __forceinline__ void load_run(const Epilogue& e, const void* base, int64_t ld, int m, int n, float (&r)[V]) {
+// Two values of a 16-bit type.
+__device__ __forceinline__ float2 unpack2(uint32_t w, int type) {
+    if (type == MPE_TYPE_BF16) {
+        __nv_bfloat162 v;
+        memcpy(&v, &w, 4);
+        return __bfloat1622float2(v);
+    }
+    __half2 v;
+    memcpy(&v, &w, 4);
+    return __half22float2(v);
+}
+
+// Four values of row m from column n on (n a multiple of 4), those below N.
+__device__ __forceinline__ void load_run(const Epilogue& e, const void* base, int64_t ld, int m, int n, float (&r)[4]) {
     const size_t at = (size_t)m * ld + n;
-    if (e.vec && n + V <= e.N) {
+    if (e.vec && n + 4 <= e.N) {
         if (e.out_type == MPE_TYPE_F32) {
-            if constexpr (V == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-                r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(base) + at);
-                r[0] = v.x, r[1] = v.y;
-            }
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+            r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
         } else {
-            uint32_t h[V / 2];
-            if constexpr (V == 4) {
-                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
-                h[0] = v.x, h[1] = v.y;
-            } else {
-                h[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + at);
-            }
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                float2 f;
-                if (e.out_type == MPE_TYPE_BF16) f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&h[i]));
-                else f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
-                r[2 * i] = f.x;
-                r[2 * i + 1] = f.y;
-            }
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+            const float2 a = unpack2(v.x, e.out_type), b = unpack2(v.y, e.out_type);
+            r[0] = a.x, r[1] = a.y, r[2] = b.x, r[3] = b.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) r[i] = n + i < e.N ? load_as_float(base, at + i, e.out_type) : 0.0f;
+        for (int i = 0; i < 4; ++i) r[i] = n + i < e.N ? load_as_float(base, at + i, e.out_type) : 0.0f;
     }
 }
 
@@ -91,23 +95,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
     return r;
 }
 
-template <int V>
-__device__ __forceinline__ void store_run(const Epilogue& e, int m, int n, const float (&r)[V]) {
+__device__ __forceinline__ void store_run(const Epilogue& e, int m, int n, const float (&r)[4]) {
     const size_t at = (size_t)m * e.ldo + n;
-    if (e.vec && n + V <= e.N) {
-        if (e.out_type == MPE_TYPE_F32) {
-            float* p = static_cast<float*>(e.out) + at;
-            if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
-            else *reinterpret_cast<float2*>(p) = make_float2(r[0], r[1]);
-        } else {
-            uint16_t* p = static_cast<uint16_t*>(e.out) + at;
-            if constexpr (V == 4)
-                *reinterpret_cast<uint2*>(p) = make_uint2(pack2(r[0], r[1], e.out_type), pack2(r[2], r[3], e.out_type));
-            else *reinterpret_cast<uint32_t*>(p) = pack2(r[0], r[1], e.out_type);
-        }
+    if (e.vec && n + 4 <= e.N) {
+        if (e.out_type == MPE_TYPE_F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(e.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(e.out) + at) =
+                make_uint2(pack2(r[0], r[1], e.out_type), pack2(r[2], r[3], e.out_type));
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < 4; ++i) {
             if (n + i >= e.N) break;
             if (e.out_type == MPE_TYPE_F32) static_cast<float*>(e.out)[at + i] = r[i];
             else if (e.out_type == MPE_TYPE_BF16) static_cast<__nv_bfloat16*>(e.out)[at + i] = __float2bfloat16_rn(r[i]);
@@ -116,69 +114,86 @@ __device__ __forceinline__ void store_run(const Epilogue& e, int m, int n, const
     }
 }
 
-// out[m, n .. n + V - 1] from the product's sums v (and the up projection's, u).
-template <int V, bool GATED>
-__device__ __forceinline__ void finish(const Epilogue& e, int m, int n, float (&v)[V], const float (&u)[V]) {
+// out[m, n .. n + 3] from the product's sums v (and the up projection's, u).
+template <bool GATED>
+__device__ __forceinline__ void finish(const Epilogue& e, int m, int n, float (&v)[4], float (&u)[4]) {
     if (n >= e.N) return;
-    float r[V];
-    if (e.residual) load_run<V>(e, e.residual, e.ldr, m, n, r);
+    float r[4];
+    if (e.residual) load_run(e, e.residual, e.ldr, m, n, r);
+    if (e.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float up = u[i];
-        if (e.bias && n + i < e.N) {
+        for (int i = 0; i < 4; ++i) {
+            if (n + i >= e.N) break;
             v[i] += load_as_float(e.bias, n + i, e.bias_type);
-            if (GATED) up += load_as_float(e.bias, (size_t)e.N + n + i, e.bias_type);
+            if (GATED) u[i] += load_as_float(e.bias, (size_t)e.N + n + i, e.bias_type);
         }
-        v[i] = activate(v[i], e.act);
-        if (GATED) v[i] *= up;
+    }
+    activate<4>(v, e.act);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (GATED) v[i] *= u[i];
         if (e.residual) v[i] += r[i];
     }
-    store_run<V>(e, m, n, v);
+    store_run(e, m, n, v);
 }
 
 // ---------------------------------------------------------------------------
 // Few tokens: the weights stream once, their rows are the MMA's M
 // ---------------------------------------------------------------------------
-// One CTA multiplies 128 rows of w (gated: 64 of the gate's and the same 64 of
-// the up projection's) with NT tokens over a share of K; the CTAs of a cluster
-// share K, leave their sums in their own shared memory, and each adds up and
-// finishes every S-th token of the tile in the order of the ranks, so that the
-// result does not depend on timing and no workspace is needed.
-//   warp 0   loads: per step of 64 inputs one box of w (gated: two) and one of x
+// One CTA multiplies 128 rows of w (gated: 64 of the gate's and the same outputs'
+// 64 of the up projection's) with NT tokens over a share of K; the S CTAs of a
+// cluster share K. Each copies its sums of a token to the CTA that finishes it,
+// where they are added up in the order of the ranks: no workspace, and a result
+// that does not depend on timing.
+//   warp 0   loads: per step of 64 inputs a box of w (gated: two) and one of x
 //   warp 1   MMAs, M = 128, N = NT
-//   all      tensor memory -> shared memory, sum over the cluster, epilogue
+//   all      tensor memory -> shared memory, sums, epilogue
+// What the next launch can do before this one has ended: its CTAs start where
+// shared memory is left, and bring their weights into L2.
 constexpr int kKStep = 64;
 constexpr int kRows = 128;
+constexpr int kAhead = 8;  // steps of w brought into L2 before earlier kernels have ended
 
 template <int NT>
 struct Narrow {
+    static constexpr int kThreads = NT <= 32 ? 128 : 256;
     static constexpr int kStageBytes = (kRows + NT) * 128;
-    static constexpr int kStages = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : NT <= 128 ? 3 : 4;
-    static constexpr int kPartBytes = NT * kRows * 4;
-    static constexpr int kRing = kStages * kStageBytes > kPartBytes ? kStages * kStageBytes : kPartBytes;
-    static constexpr int kSmem = 1024 + kRing + 256;
+    static constexpr int kStages = NT == 128 ? 5 : NT == 64 ? 3 : 4;
+    static constexpr int kRing = kStages * kStageBytes;  // then the sums, [token][row]
+    static constexpr int kPart = NT * kRows * 4;
+    static_assert(kPart <= kRing, "the sums take the ring's place");
+    // what the other ranks send: [rank][token][row], S ceil(NT / S) tokens
+    static constexpr int kSmem = 1024 + kRing + kPart + 256;
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static constexpr int kCols = NT < 32 ? 32 : NT;
 };
 
-template <int NT, bool GATED>
-__global__ void __launch_bounds__(128)
+template <int NT, int S, bool GATED>
+__global__ void __launch_bounds__(Narrow<NT>::kThreads)
 k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Epilogue e,
          const int nk, const uint32_t idesc) {
     using C = Narrow<NT>;
+    static_assert(NT % S == 0, "tokens of a rank");
+    constexpr int kOut = GATED ? kRows / 2 : kRows;  // outputs of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kRing);
+    float* part = reinterpret_cast<float*>(ring);
+    float* sent = reinterpret_cast<float*>(ring + C::kRing);
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kRing + C::kPart);
     uint64_t* empty = full + C::kStages;
     uint64_t* done = empty + C::kStages;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* got = done + 1;  // the other ranks' sums are here
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(got + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t S;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
-    const uint32_t rank = tc::cluster_rank();
-    const int n0 = (int)(blockIdx.x / S) * (GATED ? kRows / 2 : kRows);
+    const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
+    const int n0 = (int)(blockIdx.x / S) * kOut;
     const int m0 = (int)blockIdx.y * NT;
     const int k_first = (int)((int64_t)nk * rank / S), k_last = (int)((int64_t)nk * (rank + 1) / S);
+    // token t of the tile's mt is finished by rank t / per
+    const int mt = min(NT, e.M - m0);
+    const int per = (mt + S - 1) / S;
+    const int mine = max(0, min(per, mt - rank * per));
 
     if (threadIdx.x == 0) {
         tc::prefetch_map(&map_w);
@@ -188,9 +203,18 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
             mbar_init(&empty[i], 1);
         }
         mbar_init(done, 1);
+        mbar_init(got, 1);
         fence_mbar_init();
+        if (S > 1) mbar_arrive_expect_tx(got, (uint32_t)((S - 1) * mine * kRows * 4));
     }
     __syncthreads();
+    if (S > 1) tc::cluster_arrive();  // this CTA runs, and its barriers are set up
+    // L2 holds what memory holds, whoever writes it later: no need to wait here
+    if (warp == 2 && lane == 0)
+        for (int k = k_first; k < min(k_last, k_first + kAhead); ++k) {
+            tc::prefetch_box(&map_w, kKStep * k, n0);
+            if (GATED) tc::prefetch_box(&map_w, kKStep * k, e.N + n0);
+        }
     griddep_wait();
     bool ok = true;
     if (warp == 0) {
@@ -204,12 +228,8 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
                 }
                 const uint32_t dst = smem_u32(ring + s * C::kStageBytes);
                 mbar_arrive_expect_tx(&full[s], (uint32_t)C::kStageBytes);
-                if (GATED) {
-                    tc::load_box(dst, &map_w, kKStep * k, n0, &full[s]);
-                    tc::load_box(dst + kRows / 2 * 128, &map_w, kKStep * k, e.N + n0, &full[s]);
-                } else {
-                    tc::load_box(dst, &map_w, kKStep * k, n0, &full[s]);
-                }
+                tc::load_box(dst, &map_w, kKStep * k, n0, &full[s]);
+                if (GATED) tc::load_box(dst + kRows / 2 * 128, &map_w, kKStep * k, e.N + n0, &full[s]);
                 tc::load_box(dst + kRows * 128, &map_x, kKStep * k, m0, &full[s]);
                 if (++s == C::kStages) s = 0, phase ^= 1u;
             }
@@ -250,50 +270,66 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
     ok &= mbar_wait_bounded(done, 0);
     tc::fence_after();
     ok = __syncthreads_and(ok);
-    if (!ok && threadIdx.x == 0) set_status(&g_status, MPE_STATUS_WAIT_TIMEOUT);
-    // sums of this share of K, token-major: part[token][row]
-    float* part = reinterpret_cast<float*>(ring);
+    // the sums of this share of K in the ring's place: warps w and w + 4 read lanes
+    // 32 (w % 4) .., every second 16 tokens each
     const uint32_t tbase = *tmem_slot;
-    const int mt = min(NT, e.M - m0);
     if (ok) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        float* to = part + (warp & 3) * 32 + lane;
 #pragma unroll 1
-        for (int c = 0; c < mt; c += 16) {
-            uint32_t r[16];
-            tc::tmem_load16(tbase + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, r);
+        for (int c = (warp >> 2) * 16; c < mt; c += C::kThreads / 8) {
+            uint32_t v[16];
+            tc::tmem_load16(tbase + lanes + (uint32_t)c, v);
             tc::tmem_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(c + i) * kRows + threadIdx.x] = __uint_as_float(r[i]);
+            for (int i = 0; i < 16; ++i) to[(c + i) * kRows] = __uint_as_float(v[i]);
         }
     }
     tc::fence_before();
-    if (S > 1) tc::cluster_sync();
-    else __syncthreads();
+    if (S > 1) {
+        fence_proxy_async_smem();
+        __syncthreads();
+        tc::cluster_wait();
+        // one thread a rank: its tokens' sums to it
+        if ((int)threadIdx.x < S && (int)threadIdx.x != rank) {
+            const int to = threadIdx.x, n = max(0, min(per, mt - to * per));
+            if (n > 0)
+                tc::copy_to_peer(tc::peer_addr(smem_u32(sent + rank * per * kRows), to), part + to * per * kRows,
+                                 (uint32_t)(n * kRows * 4), tc::peer_addr(smem_u32(got), to));
+        }
+        if (!mbar_wait_bounded(got, 0)) ok = false;
+        __syncwarp();
+        tc::cluster_arrive();  // nothing is on its way to this CTA any more
+    } else {
+        __syncthreads();
+    }
+    if (!ok && lane == 0) set_status(&g_status, MPE_STATUS_WAIT_TIMEOUT);
     if (warp == 1) {
         tc::fence_after();
         tc::tmem_free(tbase, C::kCols);
     }
-    // every S-th token, one warp each; a lane has 4 outputs (gated: 2)
-    constexpr int V = GATED ? 2 : 4;
-    const uint32_t mine = smem_u32(part);
-    for (int t = (int)rank + (int)S * warp; t < mt; t += 4 * (int)S) {
-        float v[V], u[V];
+    // this rank's tokens, four neighbouring outputs of one at a time
+    constexpr int kRuns = kOut / 4;
+    const float* own = part + rank * per * kRows;
+    for (int it = threadIdx.x; it < mine * kRuns; it += C::kThreads) {
+        const int t = it / kRuns, r = it % kRuns * 4;
+        float4 v4[S], u4[S];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = u[i] = 0.0f;
-        const uint32_t at = mine + (uint32_t)(t * kRows + V * lane) * 4;
-#pragma unroll 8
-        for (uint32_t s = 0; s < S; ++s) {
-            const uint32_t p = tc::peer_addr(at, s);
-            if constexpr (GATED) {
-                const float2 g = tc::peer_load2(p), w = tc::peer_load2(p + kRows / 2 * 4);
-                v[0] += g.x, v[1] += g.y, u[0] += w.x, u[1] += w.y;
-            } else {
-                const float4 g = tc::peer_load4(p);
-                v[0] += g.x, v[1] += g.y, v[2] += g.z, v[3] += g.w;
-            }
+        for (int s = 0; s < S; ++s) {
+            const float* at = (S == 1 || s == rank ? own : sent + s * per * kRows) + t * kRows + r;
+            v4[s] = *reinterpret_cast<const float4*>(at);
+            if (GATED) u4[s] = *reinterpret_cast<const float4*>(at + kOut);
         }
-        finish<V, GATED>(e, m0 + t, n0 + V * lane, v, u);
+        float v[4] = {v4[0].x, v4[0].y, v4[0].z, v4[0].w}, u[4] = {};
+        if (GATED) tc::add4(u, u4[0]);
+#pragma unroll
+        for (int s = 1; s < S; ++s) {
+            tc::add4(v, v4[s]);
+            if (GATED) tc::add4(u, u4[s]);
+        }
+        finish<GATED>(e, m0 + rank * per + t, n0 + r, v, u);
     }
-    if (S > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
+    if (S > 1) tc::cluster_wait();  // the other ranks have what this one sent
 }
 
 // ---------------------------------------------------------------------------
@@ -368,15 +404,28 @@ __device__ __forceinline__ void move_rows(uint8_t* stage, void* base, int64_t ld
             }
         }
     } else {
-        for (int r = 0; r < 32 && m + r < M; ++r)
+        // 8 rows at a time, so that their loads are in flight together
+        constexpr int kC = kCols / 32;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32 && m + r0 < M; r0 += 8) {
+            V v[8][kC];
 #pragma unroll
-            for (int c = lane; c < kCols; c += 32) {
-                if (n + c >= N) continue;
-                V* p = g + (size_t)(m + r) * ld + n + c;
-                V* s = reinterpret_cast<V*>(staged(stage, r, c / kPer)) + c % kPer;
-                if (STORE) *p = *s;
-                else *s = *p;
-            }
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int h = 0; h < kC; ++h) {
+                    const int r = r0 + i, c = lane + 32 * h;
+                    if (STORE) v[i][h] = reinterpret_cast<const V*>(staged(stage, r, c / kPer))[c % kPer];
+                    else if (m + r < M && n + c < N) v[i][h] = g[(size_t)(m + r) * ld + n + c];
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int h = 0; h < kC; ++h) {
+                    const int r = r0 + i, c = lane + 32 * h;
+                    if (!STORE) reinterpret_cast<V*>(staged(stage, r, c / kPer))[c % kPer] = v[i][h];
+                    else if (m + r < M && n + c < N) g[(size_t)(m + r) * ld + n + c] = v[i][h];
+                }
+        }
     }
 }
 
@@ -520,7 +569,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                     move_rows<SZ, false>(stage, const_cast<void*>(e.residual), e.ldr, m, n0 + c, e.M, e.N, e.vec, lane);
                     __syncwarp();
                 }
-#pragma unroll
+#pragma unroll 1  // the activations' code once, not once every 16 outputs
                 for (int h = 0; h < kChunk; h += 16) {
                     uint32_t v[16], u[16];
                     tc::tmem_load16(acc + (uint32_t)(c + h), v);
@@ -531,8 +580,12 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                     for (int i = 0; i < 16; ++i) {
                         f[i] = __uint_as_float(v[i]);
                         if (e.bias) f[i] += bias[c + h + i];
-                        f[i] = activate(f[i], e.act);
-                        if (GATED) f[i] *= __uint_as_float(u[i]) + (e.bias ? bias[kOut + c + h + i] : 0.0f);
+                    }
+                    activate<16>(f, e.act);
+                    if (GATED) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            f[i] *= __uint_as_float(u[i]) + (e.bias ? bias[kOut + c + h + i] : 0.0f);
                     }
 #pragma unroll
                     for (int j = 0; j < SZ; ++j) {  // 16 SZ bytes in pieces of 16
@@ -552,16 +605,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                             } else {
                                 float lo = f[j * kPer + 2 * i], hi = f[j * kPer + 2 * i + 1];
                                 if (e.residual) {
-                                    float2 o;
-                                    if (e.out_type == MPE_TYPE_BF16) {
-                                        __nv_bfloat162 x2;
-                                        memcpy(&x2, &w[i], 4);
-                                        o = __bfloat1622float2(x2);
-                                    } else {
-                                        __half2 x2;
-                                        memcpy(&x2, &w[i], 4);
-                                        o = __half22float2(x2);
-                                    }
+                                    const float2 o = unpack2(w[i], e.out_type);
                                     lo += o.x;
                                     hi += o.y;
                                 }
@@ -624,46 +668,49 @@ bool encode(CUtensorMap* map, const void* base, int type, int64_t rows, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool GATED>
-cudaError_t launch_narrow(const mpe_linear_args& p, const Epilogue& e, int split, cudaStream_t st) {
+template <int NT, int S, bool GATED>
+cudaError_t launch_narrow(const mpe_linear_args& p, const Epilogue& e, cudaStream_t st) {
     using C = Narrow<NT>;
+    constexpr int kOut = GATED ? kRows / 2 : kRows;
     alignas(64) CUtensorMap mw, mx;
     const int64_t wrows = GATED ? 2 * (int64_t)p.N : p.N;
-    if (!encode(&mw, p.w, p.type, wrows, p.K, p.ldw, GATED ? kRows / 2 : kRows) ||
-        !encode(&mx, p.x, p.type, p.M, p.K, p.ldx, NT))
+    if (!encode(&mw, p.w, p.type, wrows, p.K, p.ldw, kOut) || !encode(&mx, p.x, p.type, p.M, p.K, p.ldx, NT))
         return cudaErrorInvalidValue;
-    cudaError_t err = cudaFuncSetAttribute(k_narrow<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t err = cudaFuncSetAttribute(k_narrow<NT, S, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (err != cudaSuccess) return err;
-    const int per = GATED ? kRows / 2 : kRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.N + per - 1) / per * split), (unsigned)((p.M + NT - 1) / NT));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)((p.N + kOut - 1) / kOut * S), (unsigned)((p.M + NT - 1) / NT));
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {(unsigned)split, 1, 1};
+    attr[1].val.clusterDim = {(unsigned)S, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_narrow<NT, GATED>, mw, mx, e, (p.K + kKStep - 1) / kKStep,
+    return cudaLaunchKernelEx(&cfg, k_narrow<NT, S, GATED>, mw, mx, e, (p.K + kKStep - 1) / kKStep,
                               tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
 }
 
+template <int NT, bool GATED>
+cudaError_t launch_narrow_split(const mpe_linear_args& p, const Epilogue& e, int split, cudaStream_t st) {
+    switch (split) {
+        case 1: return launch_narrow<NT, 1, GATED>(p, e, st);
+        case 2: return launch_narrow<NT, 2, GATED>(p, e, st);
+        case 4: return launch_narrow<NT, 4, GATED>(p, e, st);
+        default: return launch_narrow<NT, 8, GATED>(p, e, st);
+    }
+}
+
 template <bool GATED>
-cudaError_t launch_narrow_for(const mpe_linear_args& p, const Epilogue& e, cudaStream_t st, int sms) {
-    const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-    const int per = GATED ? kRows / 2 : kRows;
-    const int64_t tiles = (int64_t)((p.N + per - 1) / per) * ((p.M + nt - 1) / nt);
-    const int nk = (p.K + kKStep - 1) / kKStep;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * sms && nk >= 4 * split) split *= 2;
+cudaError_t launch_narrow_for(const mpe_linear_args& p, const Epilogue& e, int nt, int split, cudaStream_t st) {
     switch (nt) {
-        case 16: return launch_narrow<16, GATED>(p, e, split, st);
-        case 32: return launch_narrow<32, GATED>(p, e, split, st);
-        case 64: return launch_narrow<64, GATED>(p, e, split, st);
-        default: return launch_narrow<128, GATED>(p, e, split, st);
+        case 16: return launch_narrow_split<16, GATED>(p, e, split, st);
+        case 32: return launch_narrow_split<32, GATED>(p, e, split, st);
+        case 64: return launch_narrow_split<64, GATED>(p, e, split, st);
+        default: return launch_narrow_split<128, GATED>(p, e, split, st);
     }
 }
 
@@ -700,6 +747,23 @@ cudaError_t launch_wide_for(const mpe_linear_args& p, const Epilogue& e, int sms
     if (p.out_type == MPE_TYPE_F32)
         return p.gated ? launch_wide<BN, true, 4>(p, e, sms, st) : launch_wide<BN, false, 4>(p, e, sms, st);
     return p.gated ? launch_wide<BN, true, 2>(p, e, sms, st) : launch_wide<BN, false, 2>(p, e, sms, st);
+}
+
+// The kernel for a product: k_wide<tile> (wide) or k_narrow<tile, split>.
+struct Choice {
+    bool wide;
+    int tile, split;
+};
+
+Choice choose(const mpe_linear_args& p, int sms) {
+    if (p.M > 128) return {true, 256, 1};
+    const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+    const int per = p.gated ? 64 : 128;
+    const int64_t tiles = (int64_t)((p.N + per - 1) / per) * ((p.M + nt - 1) / nt);
+    const int nk = (p.K + kKStep - 1) / kKStep;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2 * sms && nk >= 4 * split) split *= 2;
+    return {false, nt, split};
 }
 
 // rows of `cols` values of sz bytes, ld values apart, as a set of bytes
@@ -769,18 +833,18 @@ extern "C" int mpe_linear(const mpe_linear_args* p, void* stream) {
     if (p->residual && !(p->residual == p->out && (p->M == 1 || p->ldr == p->ldo)) &&
         overlap(out, Block(p->residual, p->M, p->N, p->ldr, osz)))
         return report_global_errorf(MPE_ERR_INVALID, "%s: out overlaps residual without being it", who);
-    // many tokens: from two tiles of 128 on
-    const bool wide = p->M > 128;
+    const int sms = current_sm_count();
+    if (sms <= 0) return report_global_errorf(MPE_ERR_CUDA, "%s: no current device", who);
+    const Choice how = choose(*p, sms);
     // rows start where runs of 16 bytes (narrow: of 4 values) do
-    const int run = wide ? 16 : 4 * osz;
+    const int run = how.wide ? 16 : 4 * osz;
     auto runs = [&](const void* base, int64_t ld) { return aligned(base, run) && (p->M == 1 || ld * osz % run == 0); };
     const int vec = runs(p->out, p->ldo) && (!p->residual || runs(p->residual, p->ldr));
     const Epilogue e{p->bias, p->residual, p->out, p->ldr, p->ldo, p->M, p->N, p->bias_type, p->out_type, p->act, vec};
-    const int sms = current_sm_count();
-    if (sms <= 0) return report_global_errorf(MPE_ERR_CUDA, "%s: no current device", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t err = wide       ? launch_wide_for<256>(*p, e, sms, st)
-                            : p->gated ? launch_narrow_for<true>(*p, e, st, sms) : launch_narrow_for<false>(*p, e, st, sms);
+    const cudaError_t err = how.wide   ? (how.tile == 256 ? launch_wide_for<256>(*p, e, sms, st) : launch_wide_for<128>(*p, e, sms, st))
+                            : p->gated ? launch_narrow_for<true>(*p, e, how.tile, how.split, st)
+                                       : launch_narrow_for<false>(*p, e, how.tile, how.split, st);
     if (err != cudaSuccess) {
         cudaGetLastError();  // reported here, not left for the next call
         return report_global_errorf(MPE_ERR_CUDA, "%s: %s", who, cudaGetErrorString(err));
