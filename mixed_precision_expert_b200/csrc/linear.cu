@@ -281,6 +281,7 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
             uint32_t v[16];
             tc::tmem_load16(tbase + lanes + (uint32_t)c, v);
             tc::tmem_wait();
+            tc::tmem_ready(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) to[(c + i) * kRows] = __uint_as_float(v[i]);
         }
@@ -343,21 +344,21 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
 // one before is finished.
 //   warp 0     loads into a ring of K-steps of 64
 //   warp 1     MMAs (rank 0)
-//   warps 4-7  epilogue, 32 tokens each: a thread has a token's outputs, which
-//              go through 4 KB of shared memory a warp, so that global memory is
-//              read and written in runs of whole rows
+//   warps 4-11 epilogue, 32 tokens and half of the outputs each: a thread has a
+//              token's outputs, which go through 2 KB of shared memory a warp, so
+//              that global memory is read and written in runs of 64 bytes of a row
 template <int BN>
 struct Wide {
     static constexpr int kStageBytes = 128 * 128 + BN / 2 * 128;
     static constexpr int kStages = BN == 256 ? 6 : 8;
     static constexpr int kRing = kStages * kStageBytes;
-    static constexpr int kStaging = 4 * 4096;
+    static constexpr int kStaging = 8 * 2048;
     static constexpr int kSmem = 1024 + kRing + kStaging + 4 * BN * 4 + 256;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static constexpr int kCols = 2 * BN;
     static_assert(kCols <= 512, "tensor memory");
 };
-constexpr int kWideThreads = 256;
+constexpr int kWideThreads = 384;
 constexpr int kTileM = 256;
 
 struct Tiles {
@@ -374,57 +375,34 @@ __device__ __forceinline__ void tile_at(const Tiles& g, int64_t t, int& m, int& 
     m = first + (int)(in - (int64_t)n * rows);
 }
 
-// A warp's 32 rows of 128 bytes: 16-byte piece j of row r lies at j ^ (r & 7).
-__device__ __forceinline__ uint8_t* staged(uint8_t* base, int r, int j) { return base + r * 128 + ((j ^ (r & 7)) << 4); }
+// A warp's 32 rows of 64 bytes: 16-byte piece j of row r lies at j ^ (r / 2 % 4), so
+// that neither rows nor columns of pieces meet in a bank.
+__device__ __forceinline__ uint8_t* staged(uint8_t* base, int r, int j) {
+    return base + r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
+}
 
-// Between the staging rows and global rows m .. m + 31, columns n .. (128 bytes'
-// worth): 16-byte pieces where `runs`, single values otherwise.
-template <int SZ, bool STORE>
-__device__ __forceinline__ void move_rows(uint8_t* stage, void* base, int64_t ld, int m, int n, int M, int N, bool runs,
-                                          int lane) {
-    using V = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
-    constexpr int kPer = 16 / SZ, kCols = 128 / SZ;
+// Single values between the staging rows and global rows m .. m + 31, columns
+// n .. (64 bytes' worth), 8 rows at a time, so that loads are in flight together.
+template <typename V, bool STORE>
+__device__ __forceinline__ void move_values(uint8_t* stage, void* base, int64_t ld, int m, int n, int M, int N, int lane) {
+    constexpr int kPer = 16 / (int)sizeof(V), kCols = 64 / (int)sizeof(V);
+    constexpr int kRowsAt = 32 / kCols;  // rows in one pass of the warp: 1 or 2
     V* g = static_cast<V*>(base);
-    if (runs) {
-        const int j = lane & 7, c = n + j * kPer;
+    const int c = lane % kCols;
+#pragma unroll 1
+    for (int r0 = lane / kCols; r0 < 32; r0 += 8 * kRowsAt) {
+        V v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);
-            if (m + r >= M || c >= N) continue;
-            V* p = g + (size_t)(m + r) * ld + c;
-            uint8_t* s = staged(stage, r, j);
-            if (c + kPer <= N) {
-                if (STORE) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(s);
-                else *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(p);
-            } else {
-                for (int q = 0; c + q < N; ++q) {
-                    if (STORE) p[q] = reinterpret_cast<const V*>(s)[q];
-                    else reinterpret_cast<V*>(s)[q] = p[q];
-                }
-            }
+            const int r = r0 + i * kRowsAt;
+            if (STORE) v[i] = reinterpret_cast<const V*>(staged(stage, r, c / kPer))[c % kPer];
+            else if (m + r < M && n + c < N) v[i] = g[(size_t)(m + r) * ld + n + c];
         }
-    } else {
-        // 8 rows at a time, so that their loads are in flight together
-        constexpr int kC = kCols / 32;
-#pragma unroll 1
-        for (int r0 = 0; r0 < 32 && m + r0 < M; r0 += 8) {
-            V v[8][kC];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int h = 0; h < kC; ++h) {
-                    const int r = r0 + i, c = lane + 32 * h;
-                    if (STORE) v[i][h] = reinterpret_cast<const V*>(staged(stage, r, c / kPer))[c % kPer];
-                    else if (m + r < M && n + c < N) v[i][h] = g[(size_t)(m + r) * ld + n + c];
-                }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int h = 0; h < kC; ++h) {
-                    const int r = r0 + i, c = lane + 32 * h;
-                    if (!STORE) reinterpret_cast<V*>(staged(stage, r, c / kPer))[c % kPer] = v[i][h];
-                    else if (m + r < M && n + c < N) g[(size_t)(m + r) * ld + n + c] = v[i][h];
-                }
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + i * kRowsAt;
+            if (!STORE) reinterpret_cast<V*>(staged(stage, r, c / kPer))[c % kPer] = v[i];
+            else if (m + r < M && n + c < N) g[(size_t)(m + r) * ld + n + c] = v[i];
         }
     }
 }
@@ -439,11 +417,11 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* staging = ring + C::kRing;
-    float* s_bias = reinterpret_cast<float*>(staging + C::kStaging);  // [epilogue warps][BN]
+    float* s_bias = reinterpret_cast<float*>(staging + C::kStaging);  // [epilogue warps][BN / 2]
     uint64_t* full = reinterpret_cast<uint64_t*>(s_bias + 4 * BN);    // rank 0: both CTAs' boxes of a stage
     uint64_t* empty = full + C::kStages;                              // each CTA: its stage was multiplied
     uint64_t* acc_full = empty + C::kStages;                          // each CTA: [2] accumulator complete
-    uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by the 8 epilogue warps
+    uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by both CTAs' epilogue warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank();
@@ -459,7 +437,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 8);
+            mbar_init(&acc_empty[i], 16);
         }
         fence_mbar_init();
     }
@@ -539,84 +517,117 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
         }
         __syncwarp();
     } else if (warp >= 4) {
-        const int q = warp - 4;
-        uint8_t* stage = staging + q * 4096;
-        float* bias = s_bias + q * BN;
-        const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        constexpr int kChunk = 128 / SZ;  // outputs in a staging row
+        using V = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
+        constexpr int kChunk = 64 / SZ;  // outputs in a staging row
+        constexpr int kHalf = kOut / 2;  // outputs of this warp
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        uint8_t* stage = staging + (warp - 4) * 2048;
+        float* bias = s_bias + (warp - 4) * (BN / 2);  // [0, kHalf): of the outputs (the gate's); then the up projection's
+        const int row = lane >> 2, piece = lane & 3;   // of the 16-byte moves: rows row + 8 i
         int b = 0;
         uint32_t phase = 0;
         for (int64_t t = pair; t < tiles && ok; t += pairs) {
             int mt, nt;
             tile_at(grid, t, mt, nt);
-            const int m = mt * kTileM + rank * 128 + q * 32, n0 = nt * kOut;
+            const int m = mt * kTileM + rank * 128 + q * 32, n0 = nt * kOut + half * kHalf;
             if (e.bias) {
-                // [0, kOut): of the outputs (the gate's); [kOut, 2 kOut): the up projection's
-                for (int i = lane; i < BN; i += 32) {
-                    const int n = n0 + i % kOut;
-                    bias[i] = n < e.N ? load_as_float(e.bias, (size_t)(i / kOut) * e.N + n, e.bias_type) : 0.0f;
+                for (int i = lane; i < BN / 2; i += 32) {
+                    const int n = n0 + i % kHalf;
+                    bias[i] = n < e.N ? load_as_float(e.bias, (size_t)(i / kHalf) * e.N + n, e.bias_type) : 0.0f;
                 }
                 __syncwarp();
             }
+            // whole chunks move in 16-byte pieces, the residual's next one ahead
+            auto whole = [&](int c) { return e.vec && m + 32 <= e.M && n0 + c + kChunk <= e.N; };
+            const size_t at0 = (size_t)(m + row) * e.ldo + n0 + piece * (16 / SZ);
+            const size_t rt0 = (size_t)(m + row) * e.ldr + n0 + piece * (16 / SZ);
+            uint4 next[4];
+            auto fetch = [&](int c) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    next[i] = *reinterpret_cast<const uint4*>(static_cast<const V*>(e.residual) + rt0 + (size_t)(8 * i) * e.ldr + c);
+            };
+            if (e.residual && whole(0)) fetch(0);
             if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after();
-            const uint32_t acc = tbase + lanes + (uint32_t)(b * BN);
-#pragma unroll 1
-            for (int c = 0; c < kOut && ok; c += kChunk) {
+            const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + half * kHalf);
+#pragma unroll 1  // the activations' code once, not once a chunk
+            for (int c = 0; c < kHalf && ok; c += kChunk) {
                 if (n0 + c >= e.N || m >= e.M) break;
+                uint32_t v[kChunk / 16][16], u[kChunk / 16][16];
+#pragma unroll
+                for (int h = 0; h < kChunk / 16; ++h) {
+                    tc::tmem_load16(acc + (uint32_t)(c + 16 * h), v[h]);
+                    if (GATED) tc::tmem_load16(acc + (uint32_t)(kOut + c + 16 * h), u[h]);
+                }
+                const bool pieces = whole(c);
                 if (e.residual) {
-                    move_rows<SZ, false>(stage, const_cast<void*>(e.residual), e.ldr, m, n0 + c, e.M, e.N, e.vec, lane);
+                    if (pieces) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staged(stage, row + 8 * i, piece)) = next[i];
+                        if (c + kChunk < kHalf && whole(c + kChunk)) fetch(c + kChunk);
+                    } else {
+                        move_values<V, false>(stage, const_cast<void*>(e.residual), e.ldr, m, n0 + c, e.M, e.N, lane);
+                    }
                     __syncwarp();
                 }
-#pragma unroll 1  // the activations' code once, not once every 16 outputs
-                for (int h = 0; h < kChunk; h += 16) {
-                    uint32_t v[16], u[16];
-                    tc::tmem_load16(acc + (uint32_t)(c + h), v);
-                    if (GATED) tc::tmem_load16(acc + (uint32_t)(kOut + c + h), u);
-                    tc::tmem_wait();
-                    float f[16];
+                tc::tmem_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        f[i] = __uint_as_float(v[i]);
-                        if (e.bias) f[i] += bias[c + h + i];
-                    }
-                    activate<16>(f, e.act);
-                    if (GATED) {
+                for (int h = 0; h < kChunk / 16; ++h) {
+                    tc::tmem_ready(v[h]);
+                    if (GATED) tc::tmem_ready(u[h]);
+                }
+                float f[kChunk];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            f[i] *= __uint_as_float(u[i]) + (e.bias ? bias[kOut + c + h + i] : 0.0f);
-                    }
+                for (int i = 0; i < kChunk; ++i) f[i] = __uint_as_float(v[i / 16][i % 16]);
+                if (e.bias) {
 #pragma unroll
-                    for (int j = 0; j < SZ; ++j) {  // 16 SZ bytes in pieces of 16
-                        uint4* p = reinterpret_cast<uint4*>(staged(stage, lane, h * SZ / 16 + j));
-                        constexpr int kPer = 16 / SZ;
-                        uint32_t w[4];
-                        if (e.residual) {
-                            const uint4 old = *p;
-                            w[0] = old.x, w[1] = old.y, w[2] = old.z, w[3] = old.w;
-                        }
+                    for (int i = 0; i < kChunk; ++i) f[i] += bias[c + i];
+                }
+                activate<kChunk>(f, e.act);
+                if (GATED) {
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i)
+                        f[i] *= __uint_as_float(u[i / 16][i % 16]) + (e.bias ? bias[kHalf + c + i] : 0.0f);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    constexpr int kPer = 16 / SZ;
+                    uint4* p = reinterpret_cast<uint4*>(staged(stage, lane, j));
+                    if (e.residual) {
+                        const uint4 o = *p;
+                        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if constexpr (SZ == 4) {
-                                float r = f[j * kPer + i];
-                                if (e.residual) r += __uint_as_float(w[i]);
-                                w[i] = __float_as_uint(r);
+                                f[j * kPer + i] += __uint_as_float(w[i]);
                             } else {
-                                float lo = f[j * kPer + 2 * i], hi = f[j * kPer + 2 * i + 1];
-                                if (e.residual) {
-                                    const float2 o = unpack2(w[i], e.out_type);
-                                    lo += o.x;
-                                    hi += o.y;
-                                }
-                                w[i] = pack2(lo, hi, e.out_type);
+                                const float2 r = unpack2(w[i], e.out_type);
+                                f[j * kPer + 2 * i] += r.x;
+                                f[j * kPer + 2 * i + 1] += r.y;
                             }
                         }
-                        *p = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (SZ == 4) w[i] = __float_as_uint(f[j * kPer + i]);
+                        else w[i] = pack2(f[j * kPer + 2 * i], f[j * kPer + 2 * i + 1], e.out_type);
+                    }
+                    *p = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 __syncwarp();
-                move_rows<SZ, true>(stage, e.out, e.ldo, m, n0 + c, e.M, e.N, e.vec, lane);
+                if (pieces) {
+                    uint4 o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const uint4*>(staged(stage, row + 8 * i, piece));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(static_cast<V*>(e.out) + at0 + (size_t)(8 * i) * e.ldo + c) = o[i];
+                } else {
+                    move_values<V, true>(stage, e.out, e.ldo, m, n0 + c, e.M, e.N, lane);
+                }
                 __syncwarp();
             }
             tc::fence_before();

@@ -72,16 +72,11 @@ __device__ __forceinline__ V warp_max(V v) {
     return v;
 }
 
-// Keys as unsigned integers in the keys' order, +0 and -0 alike: NaN is 1,
-// -inf is above it, and 0 marks what cannot be chosen (or was).
-__device__ __forceinline__ uint32_t ordered(float f) {
-    f += 0.0f;
-    const uint32_t b = __float_as_uint(f);
-    const uint32_t u = b ^ (uint32_t)(((int32_t)b >> 31) | (int32_t)0x80000000);
-    return f == f ? u : 1u;
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+// The largest value over the warp (NaN counts as nothing).
+__device__ __forceinline__ float warp_top(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 struct SelectArgs {
@@ -154,6 +149,12 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const T* row, int 
         if (a.score == MPE_SCORE_SOFTMAX) key[i] = sum == 0.0 ? 0.0 : key[i] / sum;
         if (a.bias) key[i] += (double)a.bias[e];
     }
+    // without a bias: scores keep the logits' order, but may meet where logits do not
+    auto by_logits = [&] {
+        for (int i = 0; i < per; ++i)
+            if ((open >> i) & 1u) key[i] = (double)as_float(row[lane + 32 * i]);
+    };
+    if (!a.bias && a.group_score == MPE_GROUP_MAX) by_logits();
     if (a.keep < a.n_groups) {
         const int gs = a.E / a.n_groups;
         double mine = 0.0;  // lane g: group g's score
@@ -187,9 +188,7 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const T* row, int 
             if (e < a.E && !((kept >> (e / gs)) & 1u)) open &= ~(1u << i);
         }
     }
-    if (!a.bias)  // scores keep the logits' order, but may meet where logits do not
-        for (int i = 0; i < per; ++i)
-            if ((open >> i) & 1u) key[i] = (double)as_float(row[lane + 32 * i]);
+    if (!a.bias && a.group_score != MPE_GROUP_MAX) by_logits();
     int id = 0;
     for (int j = 0; j < a.k; ++j) {
         double v = 0.0;
@@ -209,47 +208,79 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const T* row, int 
 }
 
 // ---- the choice, one warp a token -----------------------------------------
-// Lane l holds the keys of experts l EPL .. l EPL + EPL - 1, so that the lowest
-// lane (and in it the lowest register) of equal keys is the lowest expert.
+// Lane l holds the keys of experts l EPL .. l EPL + EPL - 1. The k-th largest of
+// the lanes' largest keys is a threshold that at least k keys reach, and few
+// others (ten on the average for k = 8 of 256): the keys that reach it are moved
+// to one lane each, in the experts' order, and each lane counts the keys ahead of
+// its own. That costs a few instructions a key where k searches for a maximum
+// cost as many each. Where fewer than 2k lanes hold keys, or more than 32 keys
+// reach the threshold, k searches it is.
 //
 // Error of the float32 keys. Softmax: a term e^-d, d = m - l, carries the
 // exponential's 2 ulp (4 units of 2^-24) and the rounding of d (d units). The
 // sum of the terms adds EPL - 1 + 5 roundings and the mean of d under the
 // scores, which is at most their entropy, ln 1024 < 7; reciprocal and product
 // add 2; d s < 1/2 in the numerator. With s <= 1 that is at most EPL + 24 units.
-// Sigmoid: 2 ulp of the exponential, an addition and a reciprocal: below 2^-21.
-// Adding the bias rounds by 2^-24 |key|. Keys (or sums of two) further apart
-// than the errors of both are in float64's order; nearer ones, of which a
-// sigmoid with a bias has about one row in 2000, take select_exact.
+// Sigmoid: the fast exponential is off by 2 + 1.2 |l| ulp, which s (1 - s) <=
+// e^-|l| turns into less than 2^-23 of the score; an addition and a reciprocal
+// of 1 ulp: below 2^-21. Adding the bias rounds by 2^-24 |key|. Keys (or sums of
+// two) further apart than the errors of both are in float64's order; nearer
+// ones, of which a sigmoid with a bias has about one row in 1000, take
+// select_exact, as do rows with a NaN or an infinity in the way.
+constexpr int kSelWarps = 4;
+
+// The two largest values of several, in order.
+__device__ __forceinline__ void push2(float& m1, float& m2, float v) {
+    m2 = fmaxf(m2, fminf(m1, v));
+    m1 = fmaxf(m1, v);
+}
+
 template <typename T, int EPL>
-__global__ void __launch_bounds__(256) k_select(const SelectArgs a) {
+__global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
+    __shared__ float s_key[kSelWarps][32];
+    __shared__ int s_id[kSelWarps][32];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int warps = (gridDim.x * blockDim.x) >> 5;
     const int e0 = lane * EPL;
     const bool limited = a.keep < a.n_groups;
+    const bool sums = limited && a.group_score == MPE_GROUP_TOP2;
+    const bool softmax = a.score == MPE_SCORE_SOFTMAX;
+    const bool whole = softmax && (a.bias || sums || !a.renorm);  // the softmax's own sum is needed
     const int gs = a.E / a.n_groups;
-    for (int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < a.T; t += warps) {
+    // groups of a power of two of whole lanes: their scores by exchange
+    const int group_lanes = gs / EPL;
+    const bool by_lanes = gs % EPL == 0 && (group_lanes & (group_lanes - 1)) == 0;
+    const float err = softmax ? (EPL + 24) * 0x1p-24f : 0x1p-21f;
+    constexpr bool kHold = EPL <= 8;  // the bias stays in registers
+    float held[kHold ? EPL : 1];
+    bool nan_bias = false;
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const float b = e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.0f;
+            nan_bias |= b != b;
+            if (kHold) held[i] = b;
+        }
+        nan_bias = __any_sync(kFull, nan_bias);
+    }
+    for (int t = blockIdx.x * kSelWarps + warp; t < a.T; t += warps) {
         const T* row = static_cast<const T*>(a.logits) + (size_t)t * a.ld;
         float x[EPL];
         load_row<T, EPL>(row, a.E, a.wide, lane, x);
         // NaN, and +inf under the softmax, make the whole row's weights NaN
-        const float most = a.score == MPE_SCORE_SOFTMAX ? FLT_MAX : INFINITY;
+        const float most = softmax ? FLT_MAX : INFINITY;
         bool broken = false;
-        float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            broken |= !(x[i] <= most);
-            m = fmaxf(m, x[i]);
-        }
+        for (int i = 0; i < EPL; ++i) broken |= !(x[i] <= most);
         broken = __any_sync(kFull, broken);
-        // the softmax's maximum and sum, where something needs them
-        float inv = 0.0f;
-        const bool scores = a.bias || (limited && a.group_score == MPE_GROUP_TOP2);
-        const bool whole = a.score == MPE_SCORE_SOFTMAX && (scores || !a.renorm);
+        float m = 0.0f, inv = 0.0f;
         if (whole) {
-            m = warp_max(m);
+            m = x[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) m = fmaxf(m, x[i]);
+            m = warp_top(m);
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) sum += x[i] == -INFINITY ? 0.0f : expf(x[i] - m);
@@ -257,137 +288,222 @@ __global__ void __launch_bounds__(256) k_select(const SelectArgs a) {
             inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
         }
         auto score = [&](float l) {
-            if (a.score == MPE_SCORE_SIGMOID) return __frcp_rn(1.0f + expf(-l));
+            if (!softmax) return __fdividef(1.0f, 1.0f + __expf(-l));
             return l == -INFINITY ? 0.0f : expf(l - m) * inv;
         };
-        const float err = a.score == MPE_SCORE_SIGMOID ? 0x1p-21f : (EPL + 24) * 0x1p-24f;
-        uint32_t u[EPL];
+        float key[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const float f = a.bias ? score(x[i]) + (e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.0f) : x[i];
-            u[i] = e0 + i < a.E ? ordered(f) : 0u;
+            key[i] = x[i];
+            if (a.bias && e0 + i < a.E) key[i] = score(x[i]) + (kHold ? held[i] : __ldg(a.bias + e0 + i));
         }
-        bool close = false;
+        // -inf from here on: not to be chosen, by its key or by its group
+        bool exact = broken || nan_bias;
         if (limited) {
-            const bool sums = a.group_score == MPE_GROUP_TOP2;
-            uint32_t mine = 0;
-            float big = 0.0f;  // the largest |key| + |key| behind a finite sum
-            for (int g = 0; g < a.n_groups; ++g) {
-                // the group's two largest keys (of scores, when they are summed)
-                uint32_t m1 = 0, m2 = 0;
+            float mine = -INFINITY, big = 0.0f;  // this lane's group's score; the largest |key| + |key| in a sum
+            bool in;
+            if (by_lanes) {
+                float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    if ((unsigned)(e0 + i - g * gs) >= (unsigned)gs) continue;
-                    const uint32_t v = sums && !a.bias ? ordered(score(x[i])) : u[i];
-                    m2 = max(m2, min(m1, v));
-                    m1 = max(m1, v);
+                for (int i = 0; i < EPL; ++i)
+                    if (e0 + i < a.E) push2(m1, m2, sums && !a.bias ? score(x[i]) : key[i]);
+                for (int o = 1; o < group_lanes; o *= 2) {
+                    const float o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
+                    push2(m1, m2, o1);
+                    m2 = fmaxf(m2, o2);
                 }
-                const uint32_t b1 = __reduce_max_sync(kFull, m1);
-                uint32_t s = b1;
+                mine = m1;
                 if (sums && gs > 1) {
-                    const int owner = __ffs(__ballot_sync(kFull, m1 == b1)) - 1;
-                    const uint32_t b2 = __reduce_max_sync(kFull, lane == owner ? m2 : m1);
-                    const float f = unordered(b1) + unordered(b2);
-                    s = ordered(f);
-                    if (isfinite(f)) big = fmaxf(big, fabsf(unordered(b1)) + fabsf(unordered(b2)));
+                    mine = m1 + m2;
+                    big = isfinite(mine) ? fabsf(m1) + fabsf(m2) : 0.0f;
                 }
-                if (lane == g) mine = s;
-            }
-            int rank = 0;
-            for (int g = 0; g < a.n_groups; ++g) {
-                const uint32_t o = __shfl_sync(kFull, mine, g);
-                rank += o > mine || (o == mine && g < lane);
-            }
-            const bool in = lane < a.n_groups && rank < a.keep;
-            const uint32_t kept = __ballot_sync(kFull, in);
-            if (sums || a.bias) {
-                // the last group kept against the first one dropped
-                const float lo = unordered(__reduce_min_sync(kFull, in ? mine : ~0u));
-                const uint32_t hi_u = __reduce_max_sync(kFull, in || lane >= a.n_groups ? 0u : mine);
-                const float hi = unordered(hi_u);
-                close |= lo - hi <= 4.0f * err + 0x1p-22f * fmaxf(big, fabsf(hi));
-            }
+                const int g = lane / group_lanes;
+                int rank = 0;
+                for (int h = 0; h < a.n_groups; ++h) {
+                    const float o = __shfl_sync(kFull, mine, h * group_lanes);
+                    rank += o > mine || (o == mine && h < g);
+                }
+                exact |= __any_sync(kFull, g < a.n_groups && mine != mine);
+                in = g < a.n_groups && rank < a.keep;
+                if (sums || a.bias) {
+                    // the last group kept against the first one dropped
+                    const float lo = -warp_top(in ? -mine : -INFINITY);
+                    const float hi = warp_top(in || g >= a.n_groups ? -INFINITY : mine);
+                    exact |= lo - hi <= 4.0f * err + 0x1p-22f * fmaxf(warp_top(big), fabsf(hi));
+                }
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (e0 + i < a.E && !((kept >> ((e0 + i) / gs)) & 1u)) u[i] = 0u;
-        }
-        // k times the largest key
-        int id = 0;
-        uint32_t won = 0;
-        uint32_t top = 0;
+                for (int i = 0; i < EPL; ++i) key[i] = in ? key[i] : -INFINITY;
+            } else {
+                // lane g: group g
+                for (int g = 0; g < a.n_groups; ++g) {
+                    float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) top = max(top, u[i]);
-        for (int j = 0; j < a.k; ++j) {
-            const uint32_t best = __reduce_max_sync(kFull, top);
-            const int src = __ffs(__ballot_sync(kFull, top == best)) - 1;
-            int at = 0;
-            if (lane == src) {
-                top = 0;
-                bool taken = false;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    if (!taken && u[i] == best) {
-                        taken = true;
-                        at = e0 + i;
-                        u[i] = 0u;
+                    for (int i = 0; i < EPL; ++i)
+                        if ((unsigned)(e0 + i - g * gs) < (unsigned)gs) push2(m1, m2, sums && !a.bias ? score(x[i]) : key[i]);
+                    const float b1 = warp_top(m1);
+                    float s = b1;
+                    if (sums && gs > 1) {
+                        const int owner = __ffs(__ballot_sync(kFull, m1 == b1)) - 1;
+                        const float b2 = warp_top(lane == owner ? m2 : m1);
+                        s = b1 + b2;
+                        if (isfinite(s)) big = fmaxf(big, fabsf(b1) + fabsf(b2));
                     }
-                    top = max(top, u[i]);
+                    if (lane == g) mine = s;
+                }
+                int rank = 0;
+                for (int g = 0; g < a.n_groups; ++g) {
+                    const float o = __shfl_sync(kFull, mine, g);
+                    rank += o > mine || (o == mine && g < lane);
+                }
+                exact |= __any_sync(kFull, lane < a.n_groups && mine != mine);
+                in = lane < a.n_groups && rank < a.keep;
+                const uint32_t kept = __ballot_sync(kFull, in);
+                if (sums || a.bias) {
+                    const float lo = -warp_top(in ? -mine : -INFINITY);
+                    const float hi = warp_top(in || lane >= a.n_groups ? -INFINITY : mine);
+                    exact |= lo - hi <= 4.0f * err + 0x1p-22f * fmaxf(big, fabsf(hi));
+                }
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (e0 + i < a.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = -INFINITY;
+            }
+        }
+        // after this, lane c has the expert `id` that is number `rank` in the order (k and more: not chosen)
+        int id = 0, rank = lane;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) top = fmaxf(top, key[i]);
+        int found = 0;
+        if (!exact && 2 * a.k <= __popc(__ballot_sync(kFull, top != -INFINITY))) {
+            float rest = top, best = -INFINITY, edge = -INFINITY;
+            for (int j = 0; j < a.k; ++j) {
+                edge = warp_top(rest);
+                if (j == 0) best = edge;
+                if (rest == edge) rest = -INFINITY;
+            }
+            // -inf: lanes met in equal keys, too few are left
+            const float tol = a.bias ? 2.0f * err + 0x1p-22f * fmaxf(fabsf(best), fabsf(edge)) : 0.0f;
+            if (edge != -INFINITY) {
+                edge -= tol;
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) n += key[i] >= edge;
+                int at = n;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const int y = __shfl_up_sync(kFull, at, o);
+                    if (lane >= o) at += y;
+                }
+                found = __shfl_sync(kFull, at, 31);
+                at -= n;
+                if (found <= 32) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i)
+                        if (key[i] >= edge) {
+                            s_key[warp][at] = key[i];
+                            s_id[warp][at++] = e0 + i;
+                        }
+                    __syncwarp();
+                    const float mine = lane < found ? s_key[warp][lane] : -INFINITY;
+                    id = lane < found ? s_id[warp][lane] : 0;
+                    rank = 0;
+                    bool near = false;
+                    for (int c = 0; c < found; ++c) {
+                        const float o = s_key[warp][c];
+                        rank += o > mine || (o == mine && c < lane);
+                        near |= fabsf(o - mine) <= tol && c != lane;
+                    }
+                    if (lane >= found) rank = 32;
+                    if (a.bias && __any_sync(kFull, near && lane < found)) {
+                        // equal logits with equal biases are equal in float64 too
+                        const float l = as_float(row[id]), b = __ldg(a.bias + id);
+                        near = false;
+                        for (int c = 0; c < found; ++c) {
+                            const float o = s_key[warp][c], ol = __shfl_sync(kFull, l, c), ob = __shfl_sync(kFull, b, c);
+                            near |= fabsf(o - mine) <= tol && !(l == ol && b == ob);
+                        }
+                        exact = __any_sync(kFull, near && lane < found);
+                    }
                 }
             }
-            at = __shfl_sync(kFull, at, src);
-            if (lane == j) {
-                id = at;
-                won = best;
+        }
+        if (!exact && (found == 0 || found > 32)) {
+            // k times the largest key, of the lowest lane that has it
+            float won = 0.0f;
+            rank = lane;
+            for (int j = 0; j < a.k && !exact; ++j) {
+                const float best = warp_top(top);
+                const int src = __ffs(__ballot_sync(kFull, top == best)) - 1;
+                exact = best == -INFINITY;
+                int at = 0;
+                if (lane == src) {
+                    top = -INFINITY;
+                    bool taken = false;
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) {
+                        if (!taken && key[i] == best) {
+                            taken = true;
+                            at = e0 + i;
+                            key[i] = -INFINITY;
+                        }
+                        top = fmaxf(top, key[i]);
+                    }
+                }
+                at = __shfl_sync(kFull, at, src & 31);
+                if (lane == j) {
+                    id = at;
+                    won = best;
+                }
+            }
+            if (a.bias && !exact) {
+                // neighbours in the order that float32 cannot tell apart
+                const float l = lane < a.k ? as_float(row[id]) : 0.0f, b = lane < a.k ? __ldg(a.bias + id) : 0.0f;
+                const float pw = __shfl_up_sync(kFull, won, 1), pl = __shfl_up_sync(kFull, l, 1),
+                            pb = __shfl_up_sync(kFull, b, 1);
+                bool near = false;
+                if (lane > 0 && lane < a.k && !(l == pl && b == pb)) near = pw - won <= 2.0f * err + 0x1p-22f * fabsf(pw);
+                // and what is left against the last one chosen
+                const float lw = __shfl_sync(kFull, won, a.k - 1), ll = __shfl_sync(kFull, l, a.k - 1),
+                            lb = __shfl_sync(kFull, b, a.k - 1);
+                const float edge = lw - (2.0f * err + 0x1p-22f * fabsf(lw));
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (key[i] >= edge && !(x[i] == ll && __ldg(a.bias + e0 + i) == lb)) near = true;
+                exact = __any_sync(kFull, near);
             }
         }
-        float l = lane < a.k ? as_float(row[id]) : -INFINITY;
-        if (a.bias) {
-            // neighbours in the order that float32 cannot tell apart
-            const float key = unordered(won), b = lane < a.k ? __ldg(a.bias + id) : 0.0f;
-            const float pk = __shfl_up_sync(kFull, key, 1), pl = __shfl_up_sync(kFull, l, 1),
-                        pb = __shfl_up_sync(kFull, b, 1);
-            if (lane > 0 && lane < a.k && !(l == pl && b == pb))
-                close |= pk - key <= 2.0f * err + 0x1p-22f * fabsf(pk);
-            // and what is left against the last one chosen
-            const float lk = __shfl_sync(kFull, key, a.k - 1), ll = __shfl_sync(kFull, l, a.k - 1),
-                        lb = __shfl_sync(kFull, b, a.k - 1);
-            const float edge = 2.0f * err + 0x1p-22f * fabsf(lk);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (u[i] && lk - unordered(u[i]) <= edge && !(x[i] == ll && __ldg(a.bias + e0 + i) == lb))
-                    close = true;
-        }
-        if (__any_sync(kFull, close)) {
+        if (exact) {
             id = select_exact<T>(a, row, lane);
-            l = lane < a.k ? as_float(row[id]) : -INFINITY;
+            rank = lane;
         }
+        const bool chosen = rank < a.k;
+        const float l = chosen ? as_float(row[id]) : -INFINITY;
         // weights: of the chosen logits alone where their sum divides them
         float s = 0.0f;
         if (a.renorm) {
-            const float lm = warp_max(lane < a.k ? l : -INFINITY);
-            if (lane < a.k && l != -INFINITY) {
-                if (a.score == MPE_SCORE_SOFTMAX) s = expf(l - lm);
+            const float lm = warp_top(l);
+            if (chosen && l != -INFINITY) {
+                if (softmax) s = expf(l - lm);
                 // both factors of e^-lm where the scores may be tiny
                 else s = lm < 0.0f ? expf(l - lm) / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));
             }
             const float sum = warp_sum(s);
             s = sum == 0.0f ? 0.0f : a.scale * (s / sum);
-        } else if (lane < a.k) {
-            s = a.scale * score(l);
+        } else if (chosen) {
+            s = a.scale * (softmax ? (l == -INFINITY ? 0.0f : expf(l - m) * inv) : 1.0f / (1.0f + expf(-l)));
         }
-        if (lane < a.k) {
-            a.ids[(size_t)t * a.k + lane] = id;
-            a.w[(size_t)t * a.k + lane] = broken ? NAN : s;
+        if (chosen) {
+            a.ids[(size_t)t * a.k + rank] = id;
+            a.w[(size_t)t * a.k + rank] = broken ? NAN : s;
         }
     }
 }
 
 template <typename T, int EPL>
 cudaError_t launch_select(const SelectArgs& a, int sms, cudaStream_t st) {
-    const int block = 128;
-    const long long want = ((long long)a.T * 32 + block - 1) / block;
-    const int grid = (int)(want < (long long)sms * 16 ? want : (long long)sms * 16);
-    return launch_pdl(k_select<T, EPL>, dim3(grid), dim3(block), 0, st, a);
+    const int64_t want = ((int64_t)a.T + kSelWarps - 1) / kSelWarps, most = (int64_t)sms * 16;
+    return launch_pdl(k_select<T, EPL>, dim3((unsigned)(want < most ? want : most)), dim3(32 * kSelWarps), 0, st, a);
 }
 
 template <typename T>
@@ -419,6 +535,9 @@ struct ImportanceArgs {
 
 constexpr int kImpWarps = 16;
 
+// One warp a token, a lane's EPL columns added up in registers over the tokens;
+// then over the CTA's warps, and over the CTAs in k_importance_join, always in
+// the same order. The fast exponential: 2 + 1.2 d ulp for a score of e^-d.
 template <typename T, int EPL>
 __global__ void __launch_bounds__(32 * kImpWarps) k_importance(const ImportanceArgs a) {
     griddep_wait();
@@ -433,53 +552,52 @@ __global__ void __launch_bounds__(32 * kImpWarps) k_importance(const ImportanceA
         load_row<T, EPL>(static_cast<const T*>(a.logits) + (size_t)t * a.ld, a.E, a.wide, lane, x);
         if (a.score == MPE_SCORE_SIGMOID) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) acc[i] += __frcp_rn(1.0f + expf(-x[i]));
+            for (int i = 0; i < EPL; ++i) acc[i] += __fdividef(1.0f, 1.0f + __expf(-x[i]));
         } else {
             float m = x[0];
-            bool nan = x[0] != x[0];
 #pragma unroll
-            for (int i = 1; i < EPL; ++i) {
-                m = fmaxf(m, x[i]);
-                nan |= x[i] != x[i];
-            }
-            m = warp_max(m);
-            if (__any_sync(kFull, nan)) m = NAN;
+            for (int i = 1; i < EPL; ++i) m = fmaxf(m, x[i]);
+            m = warp_top(m);
+            if (m == -INFINITY) m = 0.0f;  // nothing but -inf: scores of 0 (and NaN stays NaN)
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                x[i] = x[i] == -INFINITY && m == m ? 0.0f : expf(x[i] - m);
+                x[i] = __expf(x[i] - m);
                 sum += x[i];
             }
             sum = warp_sum(sum);
-            const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+            const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) acc[i] += x[i] * inv;
+            for (int i = 0; i < EPL; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s_sum[warp * 32 * EPL + lane * EPL + i] = acc[i];
+    for (int i = 0; i < EPL; ++i) s_sum[(warp * EPL + i) * 32 + lane] = acc[i];
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kImpWarps; ++w) s += s_sum[w * 32 * EPL + e];
+        for (int w = 0; w < kImpWarps; ++w) s += s_sum[(w * EPL + e % EPL) * 32 + e / EPL];
         if (a.out) a.out[e] = (float)((double)s / a.T);
         else a.part[(size_t)blockIdx.x * a.E + e] = s;
     }
 }
 
-// out[e] = 1/T sum over the parts, one warp an expert.
-__global__ void __launch_bounds__(256) k_importance_join(const float* part, int parts, int E, int T,
-                                                         float* out) {
+// out[e] = 1/T sum over the parts: 32 experts a CTA, every 32nd part a warp.
+__global__ void __launch_bounds__(1024) k_importance_join(const float* part, int parts, int E, int T, float* out) {
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int e = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (e >= E) return;
+    __shared__ double s_sum[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
     double s = 0.0;
-    for (int p = lane; p < parts; p += 32) s += (double)part[(size_t)p * E + e];
-    s = warp_sum(s);
-    if (lane == 0) out[e] = (float)(s / T);
+    if (e < E)
+#pragma unroll 8
+        for (int p = warp; p < parts; p += 32) s += (double)part[(size_t)p * E + e];
+    s_sum[warp][lane] = s;
+    __syncthreads();
+    s = warp_sum(s_sum[lane][warp]);  // of expert `warp`
+    if (lane == 0 && blockIdx.x * 32 + warp < E) out[blockIdx.x * 32 + warp] = (float)(s / T);
 }
 
 // CTAs, each with sums of its own: two to an SM, and more where a warp would
@@ -601,7 +719,7 @@ extern "C" int mpe_expert_importance(const void* logits, int32_t type, int64_t l
                     : type == MPE_TYPE_BF16 ? launch_importance_t<__nv_bfloat16>(a, parts, st)
                                             : launch_importance_t<__half>(a, parts, st);
     if (e == cudaSuccess && parts > 1)
-        e = launch_pdl(k_importance_join, dim3((E + 7) / 8), dim3(256), 0, st, (const float*)a.part, parts, E,
+        e = launch_pdl(k_importance_join, dim3((E + 31) / 32), dim3(1024), 0, st, (const float*)a.part, parts, E,
                        T, p_out);
     return launched(who, e);
 }
