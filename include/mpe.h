@@ -578,16 +578,23 @@ int mpe_prefix_get_absmax(mpe_prefix* store, float* m_host);
 #define MPE_MAX_TOPK   32  /* experts chosen per token           */
 #define MPE_MAX_GROUPS 32  /* groups the choice can be limited to */
 
-typedef struct mpe_select_config {
+typedef struct mpe_select_args {
+    const void*  logits;  /* device, [T x E] of `type`, rows ld elements apart                 */
+    const float* bias;    /* device, [E], or NULL                                              */
+    int32_t*     ids;     /* device, [T x k]                                                   */
+    float*       w;       /* device, [T x k]                                                   */
+    int64_t ld;
+    int32_t T;            /* tokens (>= 0), T k <= MPE_MAX_ASSIGNMENTS                         */
     int32_t E;            /* experts, 1 .. MPE_MAX_EXPERTS                                     */
     int32_t k;            /* chosen per token, 1 .. MPE_MAX_TOPK, at most keep_groups E / n_groups */
+    int32_t type;         /* MPE_TYPE_*                                                        */
     int32_t score;        /* MPE_SCORE_*                                                       */
     int32_t n_groups;     /* 1 .. MPE_MAX_GROUPS, divides E; expert e is in group e / (E / n_groups) */
     int32_t keep_groups;  /* 1 .. n_groups                                                     */
     int32_t group_score;  /* MPE_GROUP_* (unused when every group is kept)                     */
     int32_t renormalize;  /* != 0: divide a token's weights by their sum                       */
     float   scale;        /* factor of every weight                                            */
-} mpe_select_config;
+} mpe_select_args;
 
 /*
  * mpe_select_experts -- each token's experts and weights from its router
@@ -600,38 +607,42 @@ typedef struct mpe_select_config {
  * (of groups by MPE_GROUP_MAX too) is the logits' own.
  * The choice is that of float64 scores and keys: float32 ones decide
  * wherever they are further apart than their error. Weights are float32.
- *   logits  device, [T x E] of `type` (MPE_TYPE_*), rows ld elements apart
- *   T       tokens (>= 0), T k <= MPE_MAX_ASSIGNMENTS
- *   bias    device, float32 [E], or NULL
- *   ids     device, int32 [T x k]; w device, float32 [T x k]
  * A logit of -inf has score 0 (masked), a bias of -inf bars an expert until
  * nothing else is left, and a token whose chosen scores are all 0 gets weights
  * 0 (with ids, as everywhere, in [0, E)). A NaN logit, or +inf under the
  * softmax, gives its token NaN weights; NaN keys rank lowest.
- * MPE_ERR_INVALID for a bad config, type, T, ld < E, a null pointer, or a
- * pointer that is not aligned to its elements.
+ * Rows of any alignment and pitch are taken; 16-byte aligned ones are read
+ * faster. MPE_ERR_INVALID for a size, number or type outside what the struct
+ * says, ld < E (T > 1), a null pointer, a pointer that is not aligned to its elements,
+ * or ids or w that overlap each other, the logits or the bias.
  */
-int mpe_select_experts(const mpe_select_config* cfg, const void* logits, int32_t type, int64_t ld,
-                       int32_t T, const float* bias, int32_t* ids, float* w, void* stream);
+int mpe_select_experts(const mpe_select_args* args, void* stream);
+
+typedef struct mpe_importance_args {
+    const void* logits;       /* device, [T x E] of `type`, rows ld elements apart             */
+    float*      p_out;        /* device, [E]                                                   */
+    void*       workspace;    /* device, 16-byte aligned, mpe_expert_importance_workspace(T, E)
+                                 bytes (NULL when that is 0): written by the call, free again
+                                 when the call has finished on the device                      */
+    size_t      workspace_bytes;
+    int64_t ld;
+    int32_t T;                /* tokens, >= 1                                                  */
+    int32_t E;                /* experts, 1 .. MPE_MAX_EXPERTS                                 */
+    int32_t type;             /* MPE_TYPE_*                                                    */
+    int32_t score;            /* MPE_SCORE_*                                                   */
+} mpe_importance_args;
 
 /*
  * mpe_expert_importance -- the experts' importances p_e over a batch of
  * tokens, as the width rules (mpe_allocate_bits, mpe_repage) take them: the
  * mean routing score p_e = 1/T sum_t s_{t,e} (MPE_SCORE_*). The sums' order is
  * fixed by T and E: the same input gives the same bits.
- *   logits, type, ld, T as for mpe_select_experts, with T >= 1
- *   p_out      device, float32 [E]
- *   workspace  device, 16-byte aligned, at least
- *              mpe_expert_importance_workspace(T, E) bytes (NULL when that is
- *              0); written by the call, free again when the call has finished
  * -inf logits score 0; a token of nothing else scores 0 for every expert. A
  * NaN logit makes importances NaN (its expert's under the sigmoid, all of them
  * under the softmax, as +inf does there). MPE_ERR_INVALID as for
- * mpe_select_experts, and for a workspace that is too small.
+ * mpe_select_experts, and for a workspace that is too small or overlaps.
  */
-int mpe_expert_importance(const void* logits, int32_t type, int64_t ld, int32_t T, int32_t E,
-                          int32_t score, float* p_out, void* workspace, size_t workspace_bytes,
-                          void* stream);
+int mpe_expert_importance(const mpe_importance_args* args, void* stream);
 size_t mpe_expert_importance_workspace(int32_t T, int32_t E);
 
 /* activations of mpe_linear */

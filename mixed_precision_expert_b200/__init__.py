@@ -98,7 +98,6 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, u32, u64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32,
                              ctypes.c_uint64, ctypes.c_size_t)
-    i64 = ctypes.c_int64
     sig = {
         "mpe_create": (i32, [ctypes.POINTER(vp), ctypes.POINTER(Config)]),
         "mpe_destroy": (None, [vp]),
@@ -143,8 +142,8 @@ def lib() -> ctypes.CDLL:
         "mpe_profile_enable": (i32, [vp, i32]),
         "mpe_profile_read": (i32, [vp, vp, vp, i32, i32]),
         "mpe_route_noalloc": (i32, [vp, i32, i32, i32, vp, vp, vp, vp]),
-        "mpe_select_experts": (i32, [vp, vp, i32, i64, i32, vp, vp, vp, vp]),
-        "mpe_expert_importance": (i32, [vp, i32, i64, i32, i32, i32, vp, vp, sz, vp]),
+        "mpe_select_experts": (i32, [vp, vp]),
+        "mpe_expert_importance": (i32, [vp, vp]),
         "mpe_expert_importance_workspace": (sz, [i32, i32]),
         "mpe_linear": (i32, [vp, vp]),
         "mpe_global_status": (i32, [vp, i32]),
@@ -233,63 +232,60 @@ def route_noalloc(ids, E: int, perm, offsets, inv):
 
 
 # ---- around the routed experts ------------------------------------------------
-# mpe_select_config and mpe_linear_args as packed bytes
-_SELECT_CONFIG = struct.Struct("=7if")
+# mpe_select_args, mpe_importance_args and mpe_linear_args as packed bytes
+_SELECT_ARGS = struct.Struct("=4Qq9if")
+_IMPORTANCE_ARGS = struct.Struct("=4Qq4i")
 _LINEAR_ARGS = struct.Struct("=5Q4q8i")
-_types = None
-_cuda = None  # torch's (current device, current stream's handle) queries
+_ops = None  # see _load_ops
 
 
-def _lookup():
-    """torch's types by MPE_TYPE_* and its device and stream queries (the handles that
-    torch.cuda.current_device() and current_stream() wrap, at a twentieth of their time)."""
-    global _types, _cuda
+def _load_ops():
+    """(torch's types by MPE_TYPE_*, current device, current stream of a device, the three
+    calls): the two queries are what torch.cuda.current_device() and current_stream() wrap, at
+    a twentieth of their time."""
+    global _ops
     import torch
-    _types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
     torch.cuda.current_device()  # initialises CUDA
-    _cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    L = lib()
+    _ops = ({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16},
+            torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+            L.mpe_select_experts, L.mpe_expert_importance, L.mpe_linear)
+    return _ops
 
 
-def _call(f, dev: int, *args):
-    """f(*args, stream) on device `dev` and its current stream."""
-    device, stream = _cuda
-    if dev == device():
-        rc = f(*args, stream(dev))
-    else:
-        import torch
-        with torch.cuda.device(dev):
-            rc = f(*args, stream(dev))
-    if rc != MPE_OK:
-        _check(rc)
+def _on(dev: int, f, args: bytes):
+    """f(args, stream) for a device other than the current one."""
+    import torch
+    with torch.cuda.device(dev):
+        return f(args, torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _device(t) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if _cuda is None:
-        _lookup()
     return dev
 
 
-def _type(t, what: str) -> int:
-    typ = _types.get(t.dtype)
+def _type(types, t, what: str) -> int:
+    typ = types.get(t.dtype)
     if typ is None:
         raise ValueError(f"{what} must be float32, bfloat16 or float16, not {t.dtype}")
     return typ
 
 
 def _matrix(t, what: str, dev: int):
-    """((rows, columns), pitch) of a matrix with contiguous rows on device dev."""
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{what} must be a matrix")
-    pitch, step = t.stride()
-    if step != 1 and shape[1] > 1:
-        raise ValueError(f"{what} must have contiguous rows")
+    """(rows, columns, pitch) of a matrix with contiguous rows on device dev."""
     if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, not on CUDA device {dev}")
-    return shape, pitch
+    try:
+        rows, cols = t.shape
+    except ValueError:
+        raise ValueError(f"{what} must be a matrix") from None
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return rows, cols, pitch
 
 
 def _vector(t, n: int, what: str, dev: int, dtypes):
@@ -311,22 +307,29 @@ def select_experts(logits, k: int, *, bias=None, score: int = SCORE_SOFTMAX, n_g
     their sum with ``renormalize``, times ``scale`` (mpe_select_experts). Current stream."""
     import torch
     dev = _device(logits)
-    (T, E), ld = _matrix(logits, "logits", dev)
-    typ = _type(logits, "logits")
+    types, device, stream, f, _, _ = _ops or _load_ops()
+    T, E, ld = _matrix(logits, "logits", dev)
+    bptr = 0
     if bias is not None:
         _vector(bias, E, "bias", dev, (torch.float32,))
+        bptr = bias.data_ptr()
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    elif ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous() or ids.get_device() != dev:
+    elif (ids.dtype != torch.int32 or ids.shape != (T, k) or not ids.is_contiguous()
+          or ids.get_device() != dev):
         raise ValueError(f"ids must be a contiguous int32 [{T}, {k}] on CUDA device {dev}")
     if w is None:
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    elif w.shape != (T, k) or w.dtype != torch.float32 or not w.is_contiguous() or w.get_device() != dev:
+    elif (w.dtype != torch.float32 or w.shape != (T, k) or not w.is_contiguous()
+          or w.get_device() != dev):
         raise ValueError(f"w must be a contiguous float32 [{T}, {k}] on CUDA device {dev}")
-    cfg = _SELECT_CONFIG.pack(E, k, score, n_groups, n_groups if keep_groups is None else keep_groups,
-                              group_score, 1 if renormalize else 0, scale)
-    _call(lib().mpe_select_experts, dev, cfg, logits.data_ptr(), typ, ld if T > 1 else max(ld, E), T,
-          0 if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr())
+    args = _SELECT_ARGS.pack(logits.data_ptr(), bptr, ids.data_ptr(), w.data_ptr(), ld, T, E, k,
+                             _type(types, logits, "logits"), score, n_groups,
+                             n_groups if keep_groups is None else keep_groups, group_score,
+                             1 if renormalize else 0, scale)
+    rc = f(args, stream(dev)) if dev == device() else _on(dev, f, args)
+    if rc != MPE_OK:
+        _check(rc)
     return ids, w
 
 
@@ -336,17 +339,19 @@ def expert_importance(logits, *, score: int = SCORE_SOFTMAX, out=None):
     Current stream."""
     import torch
     dev = _device(logits)
-    (T, E), ld = _matrix(logits, "logits", dev)
-    typ = _type(logits, "logits")
+    types, device, stream, _, f, _ = _ops or _load_ops()
+    T, E, ld = _matrix(logits, "logits", dev)
     if out is None:
         out = torch.empty(E, dtype=torch.float32, device=logits.device)
     else:
         _vector(out, E, "out", dev, (torch.float32,))
-    L = lib()
-    need = L.mpe_expert_importance_workspace(T, E)
+    need = lib().mpe_expert_importance_workspace(T, E)
     ws = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
-    _call(L.mpe_expert_importance, dev, logits.data_ptr(), typ, ld if T > 1 else max(ld, E), T, E, score,
-          out.data_ptr(), ws.data_ptr() if need else 0, need)
+    args = _IMPORTANCE_ARGS.pack(logits.data_ptr(), out.data_ptr(), ws.data_ptr() if need else 0, need, ld,
+                                 T, E, _type(types, logits, "logits"), score)
+    rc = f(args, stream(dev)) if dev == device() else _on(dev, f, args)
+    if rc != MPE_OK:
+        _check(rc)
     return out
 
 
@@ -358,36 +363,40 @@ def linear(x, weight, *, bias=None, act: int = ACT_NONE, gated: bool = False, re
     of x's type or float32, out (and residual, which may be ``out`` itself) of x's type or
     float32 (``out_dtype``, default the residual's or x's) (mpe_linear). Current stream."""
     dev = _device(x)
-    (M, K), ldx = _matrix(x, "x", dev)
-    (R, Kw), ldw = _matrix(weight, "weight", dev)
-    typ = _type(x, "x")
-    if Kw != K or weight.dtype != x.dtype:
-        raise ValueError(f"weight must be {x.dtype} [N, {K}]")
+    types, device, stream, _, _, f = _ops or _load_ops()
+    M, K, ldx = _matrix(x, "x", dev)
+    R, Kw, ldw = _matrix(weight, "weight", dev)
+    dtype = x.dtype
+    if Kw != K or weight.dtype != dtype:
+        raise ValueError(f"weight must be {dtype} [N, {K}]")
     if gated and R % 2:
         raise ValueError("a gated weight has an even number of rows")
     N = R // 2 if gated else R
     bptr = btyp = rptr = ldr = 0
     if bias is not None:
         import torch
-        _vector(bias, R, "bias", dev, (x.dtype, torch.float32))
-        bptr, btyp = bias.data_ptr(), _type(bias, "bias")
+        _vector(bias, R, "bias", dev, (dtype, torch.float32))
+        bptr, btyp = bias.data_ptr(), types[bias.dtype]
     if out is None:
         import torch
-        out = torch.empty((M, N), dtype=out_dtype or (x.dtype if residual is None else residual.dtype),
+        out = torch.empty((M, N), dtype=out_dtype or (dtype if residual is None else residual.dtype),
                           device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
-    shape, ldo = _matrix(out, "out", dev)
-    if shape != (M, N):
+    mo, no, ldo = _matrix(out, "out", dev)
+    if mo != M or no != N:
         raise ValueError(f"out must be [{M}, {N}]")
     if residual is not None:
-        shape, ldr = _matrix(residual, "residual", dev)
-        if shape != (M, N) or residual.dtype != out.dtype:
+        mo, no, ldr = _matrix(residual, "residual", dev)
+        if mo != M or no != N or residual.dtype != out.dtype:
             raise ValueError(f"residual must be {out.dtype} [{M}, {N}]")
         rptr = residual.data_ptr()
     args = _LINEAR_ARGS.pack(x.data_ptr(), weight.data_ptr(), bptr, rptr, out.data_ptr(), ldx, ldw, ldr, ldo,
-                             M, N, K, typ, btyp, _type(out, "out"), act, 1 if gated else 0)
-    _call(lib().mpe_linear, dev, args)
+                             M, N, K, _type(types, x, "x"), btyp, _type(types, out, "out"), act,
+                             1 if gated else 0)
+    rc = f(args, stream(dev)) if dev == device() else _on(dev, f, args)
+    if rc != MPE_OK:
+        _check(rc)
     return out
 
 

@@ -26,4 +26,27 @@ inline int current_sm_count() {
     return n;
 }
 
+// rows of `cols` values of sz bytes, ld values apart, as a set of bytes
+struct Block {
+    uintptr_t base;
+    int64_t pitch, width, rows;
+    Block(const void* p, int64_t r, int64_t cols, int64_t ld, int sz)
+        : base(reinterpret_cast<uintptr_t>(p)), pitch(r > 1 ? ld * sz : cols * sz), width(cols * sz), rows(r) {}
+    uintptr_t end() const { return base + (uintptr_t)((rows - 1) * pitch + width); }
+};
+
+// Whether two blocks share a byte. Blocks of one pitch whose spans interleave
+// (columns of one buffer) share none when their columns do not meet; blocks of
+// different pitches count as overlapping when their spans do.
+inline bool overlap(const Block& p, const Block& q) {
+    if (p.end() <= q.base || q.end() <= p.base) return false;
+    if (p.rows > 1 && q.rows > 1 && p.pitch == q.pitch) {
+        // where q's rows start in p's
+        const int64_t at = q.base >= p.base ? (int64_t)(q.base - p.base) % p.pitch
+                                            : (p.pitch - (int64_t)(p.base - q.base) % p.pitch) % p.pitch;
+        return at < p.width || at + q.width > p.pitch;
+    }
+    return true;
+}
+
 }  // namespace mpe

@@ -26,34 +26,48 @@ __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
 
-// Lane `lane`'s EPL consecutive values of a row of E (-inf past its end).
-// `wide`: the row starts on a 16-byte boundary and E is a multiple of EPL, so
-// that a lane's values are one aligned run, all inside or all outside.
+// A lane's EPL consecutive values from `row` on, the first n of them (-inf after
+// those). `wide`: `row` is aligned to the pieces of up to 16 bytes that are loaded.
+template <int BYTES>
+struct Piece;
+template <>
+struct Piece<16> { using type = uint4; };
+template <>
+struct Piece<8> { using type = uint2; };
+template <>
+struct Piece<4> { using type = uint32_t; };
+template <>
+struct Piece<2> { using type = uint16_t; };
+
 template <typename T, int EPL>
-__device__ __forceinline__ void load_row(const T* row, int E, bool wide, int lane, float (&x)[EPL]) {
-    const int e0 = lane * EPL;
-    constexpr int kBytes = EPL * (int)sizeof(T);
-    if constexpr (kBytes % 16 == 0) {
-        if (wide) {
-            if (e0 < E) {
-                constexpr int kPer = 16 / (int)sizeof(T);
+__host__ __device__ constexpr int piece_bytes() {
+    return EPL * (int)sizeof(T) < 16 ? EPL * (int)sizeof(T) : 16;
+}
+
+template <typename T, int EPL>
+__device__ __forceinline__ void load_row(const T* row, int n, bool wide, float (&x)[EPL]) {
+    if (wide) {
+        using P = typename Piece<piece_bytes<T, EPL>()>::type;
+        constexpr int kPer = (int)(sizeof(P) / sizeof(T));
 #pragma unroll
-                for (int i = 0; i < kBytes / 16; ++i) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + i);
-                    T t[kPer];
-                    memcpy(t, &v, 16);
+        for (int i = 0; i < EPL; i += kPer) {
+            T t[kPer];
+            P v;
+            const bool all = i + kPer <= n;
+            if (all) v = __ldg(reinterpret_cast<const P*>(row + i));
+            memcpy(t, &v, sizeof(P));
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) x[i * kPer + j] = as_float(t[j]);
-                }
-            } else {
+            for (int j = 0; j < kPer; ++j) x[i + j] = all ? as_float(t[j]) : -INFINITY;
+            if (!all && i < n) {  // the row's end inside a piece
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
+                for (int j = 0; j < kPer; ++j)
+                    if (i + j < n) x[i + j] = as_float(row[i + j]);
             }
-            return;
         }
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = e0 + i < E ? as_float(row[e0 + i]) : -INFINITY;
+        for (int i = 0; i < EPL; ++i) x[i] = i < n ? as_float(row[i]) : -INFINITY;
+    }
 }
 
 template <typename V>
@@ -87,8 +101,17 @@ struct SelectArgs {
     float* w;
     int T, E, k, score, n_groups, keep, group_score, renorm;
     float scale;
-    int wide;
+    // lanes: group g (the one group of all experts when every group is kept) has
+    // lanes g lanes .. (g + 1) lanes - 1, a power of two, lane i of them its experts
+    // i EPL .. i EPL + EPL - 1
+    int lanes;
+    int wide;  // every lane's run starts where its pieces of up to 16 bytes do
 };
+
+__device__ __forceinline__ double score64(double l, double m, double sum, bool softmax) {
+    if (!softmax) return 1.0 / (1.0 + exp(-l));
+    return l == -INFINITY || sum == 0.0 ? 0.0 : exp(l - m) / sum;
+}
 
 // ---- float64 choice -------------------------------------------------------
 // The same choice with float64 keys, for the rows whose float32 keys are too
@@ -207,14 +230,79 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const T* row, int 
     return id;
 }
 
+// Whether this lane's group is kept, by float64 keys: for the rows whose groups'
+// float32 scores are too close together to decide. (No NaN in the row.)
+template <typename T>
+__device__ __noinline__ bool groups_exact(const SelectArgs& a, const T* row, int lane, int group, int e0, int n, double m) {
+    const bool softmax = a.score == MPE_SCORE_SOFTMAX;
+    const int gs = a.E / a.n_groups;
+    double sum = 0.0;
+    if (softmax) {
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const double l = (double)as_float(row[e0 + i]);
+            sum += l == -INFINITY ? 0.0 : exp(l - m);
+        }
+        sum = warp_sum(sum);
+    }
+    double m1 = -INFINITY, m2 = -INFINITY;
+    auto push = [&](double v) {
+        const double less = m1 < v ? m1 : v;
+        m2 = m2 > less ? m2 : less;
+        m1 = m1 > v ? m1 : v;
+    };
+#pragma unroll 4
+    for (int i = 0; i < n; ++i)
+        push(score64((double)as_float(row[e0 + i]), m, sum, softmax) + (a.bias ? (double)a.bias[e0 + i] : 0.0));
+    for (int o = 1; o < a.lanes; o *= 2) {
+        const double o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
+        push(o1);
+        m2 = m2 > o2 ? m2 : o2;
+    }
+    const double mine = a.group_score == MPE_GROUP_TOP2 && gs > 1 ? m1 + m2 : m1;
+    int rank = 0;
+    for (int g = 0; g < a.n_groups; ++g) {
+        const double o = __shfl_sync(kFull, mine, g * a.lanes);
+        rank += o > mine || (o == mine && g < group);
+    }
+    return group < a.n_groups && rank < a.keep;
+}
+
+// This lane's place among the first `found` lanes' experts, by their float64 keys
+// (without a bias: by the logits), ties by the index.
+template <typename T>
+__device__ __noinline__ int rank_exact(const SelectArgs& a, const T* row, int e0, int n, double m, int id, int found) {
+    const bool softmax = a.score == MPE_SCORE_SOFTMAX;
+    double v = (double)as_float(row[id]);
+    if (a.bias) {
+        double sum = 0.0;
+        if (softmax) {
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const double l = (double)as_float(row[e0 + i]);
+                sum += l == -INFINITY ? 0.0 : exp(l - m);
+            }
+            sum = warp_sum(sum);
+        }
+        v = score64(v, m, sum, softmax) + (double)__ldg(a.bias + id);
+    }
+    int rank = 0;
+    for (int c = 0; c < found; ++c) {
+        const double o = __shfl_sync(kFull, v, c);
+        const int oid = __shfl_sync(kFull, id, c);
+        rank += o > v || (o == v && oid < id);
+    }
+    return rank;
+}
+
 // ---- the choice, one warp a token -----------------------------------------
-// Lane l holds the keys of experts l EPL .. l EPL + EPL - 1. The k-th largest of
-// the lanes' largest keys is a threshold that at least k keys reach, and few
-// others (ten on the average for k = 8 of 256): the keys that reach it are moved
-// to one lane each, in the experts' order, and each lane counts the keys ahead of
-// its own. That costs a few instructions a key where k searches for a maximum
-// cost as many each. Where fewer than 2k lanes hold keys, or more than 32 keys
-// reach the threshold, k searches it is.
+// A lane holds EPL experts' keys, in the experts' order over the lanes. The k-th
+// largest of the lanes' largest keys is a threshold that at least k keys reach,
+// and few others (ten on the average for k = 8 of 256): the keys that reach it
+// are moved to one lane each, and each lane counts the keys ahead of its own.
+// That costs a few instructions a key where k searches for a maximum cost as many
+// each. Where too few lanes hold keys for that, or more than 32 keys reach the
+// threshold, k searches it is.
 //
 // Error of the float32 keys. Softmax: a term e^-d, d = m - l, carries the
 // exponential's 2 ulp (4 units of 2^-24) and the rounding of d (d units). The
@@ -224,34 +312,61 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const T* row, int 
 // Sigmoid: the fast exponential is off by 2 + 1.2 |l| ulp, which s (1 - s) <=
 // e^-|l| turns into less than 2^-23 of the score; an addition and a reciprocal
 // of 1 ulp: below 2^-21. Adding the bias rounds by 2^-24 |key|. Keys (or sums of
-// two) further apart than the errors of both are in float64's order; nearer
-// ones, of which a sigmoid with a bias has about one row in 1000, take
-// select_exact, as do rows with a NaN or an infinity in the way.
+// two) further apart than the errors of both are in float64's order. Of nearer
+// keys, which a sigmoid with a bias has in one row of 1000, the order is found
+// again from their float64 values; rows with near groups, a NaN or an infinity
+// in the way take select_exact.
 constexpr int kSelWarps = 4;
 
-// The two largest values of several, in order.
+// The two largest values of several, in order (no NaN).
 __device__ __forceinline__ void push2(float& m1, float& m2, float v) {
     m2 = fmaxf(m2, fminf(m1, v));
     m1 = fmaxf(m1, v);
 }
 
+__device__ __forceinline__ float fast_rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / (1 + e^-l)
+__device__ __forceinline__ float fast_sigmoid(float l) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * l));
+    return fast_rcp(1.0f + e);
+}
+
+// The n-th largest of the lanes' values, or less where some are equal (-inf:
+// fewer than n are different); `best`: the largest.
+__device__ __forceinline__ float nth_top(float v, int n, float& best) {
+    best = warp_top(v);
+    float r = best;
+    for (int j = 1; j < n; ++j) {
+        if (v == r) v = -INFINITY;
+        r = warp_top(v);
+    }
+    return r;
+}
+
 template <typename T, int EPL>
-__global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
-    __shared__ float s_key[kSelWarps][32];
-    __shared__ int s_id[kSelWarps][32];
+__global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 : 3) k_select(const SelectArgs a) {
+    __shared__ __align__(16) float s_key[kSelWarps][32];
+    __shared__ float s_logit[kSelWarps][32];
+    __shared__ int s_id[kSelWarps][32], s_found[kSelWarps];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int warps = (gridDim.x * blockDim.x) >> 5;
-    const int e0 = lane * EPL;
     const bool limited = a.keep < a.n_groups;
     const bool sums = limited && a.group_score == MPE_GROUP_TOP2;
     const bool softmax = a.score == MPE_SCORE_SOFTMAX;
     const bool whole = softmax && (a.bias || sums || !a.renorm);  // the softmax's own sum is needed
-    const int gs = a.E / a.n_groups;
-    // groups of a power of two of whole lanes: their scores by exchange
-    const int group_lanes = gs / EPL;
-    const bool by_lanes = gs % EPL == 0 && (group_lanes & (group_lanes - 1)) == 0;
+    const int gs = limited ? a.E / a.n_groups : a.E;
+    const int group = lane / a.lanes;
+    const int from = (lane & (a.lanes - 1)) * EPL;  // in the group
+    const int e0 = group * gs + from;
+    const int n = group * gs < a.E ? max(0, min(EPL, gs - from)) : 0;
     const float err = softmax ? (EPL + 24) * 0x1p-24f : 0x1p-21f;
     constexpr bool kHold = EPL <= 8;  // the bias stays in registers
     float held[kHold ? EPL : 1];
@@ -259,7 +374,7 @@ __global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
     if (a.bias) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const float b = e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.0f;
+            const float b = i < n ? __ldg(a.bias + e0 + i) : -INFINITY;
             nan_bias |= b != b;
             if (kHold) held[i] = b;
         }
@@ -268,13 +383,20 @@ __global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
     for (int t = blockIdx.x * kSelWarps + warp; t < a.T; t += warps) {
         const T* row = static_cast<const T*>(a.logits) + (size_t)t * a.ld;
         float x[EPL];
-        load_row<T, EPL>(row, a.E, a.wide, lane, x);
+        load_row<T, EPL>(row + e0, n, a.wide, x);
         // NaN, and +inf under the softmax, make the whole row's weights NaN
         const float most = softmax ? FLT_MAX : INFINITY;
-        bool broken = false;
+        float total = x[0];  // shows either
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) broken |= !(x[i] <= most);
-        broken = __any_sync(kFull, broken);
+        for (int i = 1; i < EPL; ++i) total += x[i];
+        bool broken = __any_sync(kFull, !(total <= FLT_MAX));
+        if (broken) {
+            broken = false;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) broken |= !(x[i] <= most);
+            broken = __any_sync(kFull, broken);
+        }
+        bool exact = broken || nan_bias;
         float m = 0.0f, inv = 0.0f;
         if (whole) {
             m = x[0];
@@ -288,154 +410,114 @@ __global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
             inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
         }
         auto score = [&](float l) {
-            if (!softmax) return __fdividef(1.0f, 1.0f + __expf(-l));
+            if (!softmax) return fast_sigmoid(l);
             return l == -INFINITY ? 0.0f : expf(l - m) * inv;
         };
+        // -inf: not to be chosen, by its key or by its group
         float key[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             key[i] = x[i];
-            if (a.bias && e0 + i < a.E) key[i] = score(x[i]) + (kHold ? held[i] : __ldg(a.bias + e0 + i));
+            if (a.bias) key[i] = score(x[i]) + (kHold ? held[i] : i < n ? __ldg(a.bias + e0 + i) : -INFINITY);
         }
-        // -inf from here on: not to be chosen, by its key or by its group
-        bool exact = broken || nan_bias;
         if (limited) {
-            float mine = -INFINITY, big = 0.0f;  // this lane's group's score; the largest |key| + |key| in a sum
-            bool in;
-            if (by_lanes) {
-                float m1 = -INFINITY, m2 = -INFINITY;
+            float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (e0 + i < a.E) push2(m1, m2, sums && !a.bias ? score(x[i]) : key[i]);
-                for (int o = 1; o < group_lanes; o *= 2) {
-                    const float o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
-                    push2(m1, m2, o1);
-                    m2 = fmaxf(m2, o2);
-                }
-                mine = m1;
-                if (sums && gs > 1) {
-                    mine = m1 + m2;
-                    big = isfinite(mine) ? fabsf(m1) + fabsf(m2) : 0.0f;
-                }
-                const int g = lane / group_lanes;
-                int rank = 0;
-                for (int h = 0; h < a.n_groups; ++h) {
-                    const float o = __shfl_sync(kFull, mine, h * group_lanes);
-                    rank += o > mine || (o == mine && h < g);
-                }
-                exact |= __any_sync(kFull, g < a.n_groups && mine != mine);
-                in = g < a.n_groups && rank < a.keep;
-                if (sums || a.bias) {
-                    // the last group kept against the first one dropped
-                    const float lo = -warp_top(in ? -mine : -INFINITY);
-                    const float hi = warp_top(in || g >= a.n_groups ? -INFINITY : mine);
-                    exact |= lo - hi <= 4.0f * err + 0x1p-22f * fmaxf(warp_top(big), fabsf(hi));
-                }
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) key[i] = in ? key[i] : -INFINITY;
-            } else {
-                // lane g: group g
-                for (int g = 0; g < a.n_groups; ++g) {
-                    float m1 = -INFINITY, m2 = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i)
-                        if ((unsigned)(e0 + i - g * gs) < (unsigned)gs) push2(m1, m2, sums && !a.bias ? score(x[i]) : key[i]);
-                    const float b1 = warp_top(m1);
-                    float s = b1;
-                    if (sums && gs > 1) {
-                        const int owner = __ffs(__ballot_sync(kFull, m1 == b1)) - 1;
-                        const float b2 = warp_top(lane == owner ? m2 : m1);
-                        s = b1 + b2;
-                        if (isfinite(s)) big = fmaxf(big, fabsf(b1) + fabsf(b2));
-                    }
-                    if (lane == g) mine = s;
-                }
-                int rank = 0;
-                for (int g = 0; g < a.n_groups; ++g) {
-                    const float o = __shfl_sync(kFull, mine, g);
-                    rank += o > mine || (o == mine && g < lane);
-                }
-                exact |= __any_sync(kFull, lane < a.n_groups && mine != mine);
-                in = lane < a.n_groups && rank < a.keep;
-                const uint32_t kept = __ballot_sync(kFull, in);
-                if (sums || a.bias) {
-                    const float lo = -warp_top(in ? -mine : -INFINITY);
-                    const float hi = warp_top(in || lane >= a.n_groups ? -INFINITY : mine);
-                    exact |= lo - hi <= 4.0f * err + 0x1p-22f * fmaxf(big, fabsf(hi));
-                }
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (e0 + i < a.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = -INFINITY;
+            for (int i = 0; i < EPL; ++i) push2(m1, m2, sums && !a.bias && i < n ? score(x[i]) : key[i]);
+            for (int o = 1; o < a.lanes; o *= 2) {
+                const float o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
+                push2(m1, m2, o1);
+                m2 = fmaxf(m2, o2);
             }
+            float mine = m1, big = 0.0f;  // the group's score; |key| + |key| in a finite sum
+            if (sums && gs > 1) {
+                mine = m1 + m2;
+                big = isfinite(mine) ? fabsf(m1) + fabsf(m2) : 0.0f;
+            }
+            if (group >= a.n_groups) mine = -INFINITY;
+            // every group's score once, in the first of its lanes
+            float best, least = nth_top(from == 0 ? mine : -INFINITY, a.keep, best);
+            bool in = group < a.n_groups && mine >= least;
+            if (__popc(__ballot_sync(kFull, in && from == 0)) != a.keep) {  // equal scores
+                int rank = 0;
+                for (int g = 0; g < a.n_groups; ++g) {
+                    const float o = __shfl_sync(kFull, mine, g * a.lanes);
+                    rank += o > mine || (o == mine && g < group);
+                }
+                in = group < a.n_groups && rank < a.keep;
+                least = -warp_top(in ? -mine : -INFINITY);
+            }
+            exact |= __any_sync(kFull, mine != mine);
+            if (sums || a.bias) {
+                // the last group kept against the first one dropped
+                const float over = warp_top(in ? -INFINITY : mine);
+                if (!exact && least - over <= 4.0f * err + 0x1p-22f * fmaxf(warp_top(big), fabsf(over)))
+                    in = groups_exact<T>(a, row, lane, group, e0, n, (double)m);
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = in ? key[i] : -INFINITY;
         }
-        // after this, lane c has the expert `id` that is number `rank` in the order (k and more: not chosen)
-        int id = 0, rank = lane;
-        float top = -INFINITY;
+        // after this, a lane has the expert `id` that is number `rank` in the order (k and more: not chosen)
+        int id = 0, rank = lane, found = 0;
+        float mine = -INFINITY, l = -INFINITY;  // its key and logit
+        bool unclear = false;
+        float top = key[0];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) top = fmaxf(top, key[i]);
-        int found = 0;
-        if (!exact && 2 * a.k <= __popc(__ballot_sync(kFull, top != -INFINITY))) {
-            float rest = top, best = -INFINITY, edge = -INFINITY;
-            for (int j = 0; j < a.k; ++j) {
-                edge = warp_top(rest);
-                if (j == 0) best = edge;
-                if (rest == edge) rest = -INFINITY;
-            }
-            // -inf: lanes met in equal keys, too few are left
-            const float tol = a.bias ? 2.0f * err + 0x1p-22f * fmaxf(fabsf(best), fabsf(edge)) : 0.0f;
+        for (int i = 1; i < EPL; ++i) top = fmaxf(top, key[i]);
+        if (!exact && 3 * __popc(__ballot_sync(kFull, top != -INFINITY)) >= 4 * a.k) {
+            float best, edge = nth_top(top, a.k, best);
             if (edge != -INFINITY) {
+                __syncwarp();  // the last row's are read
+                const float tol = a.bias ? 2.0f * err + 0x1p-22f * fmaxf(fabsf(best), fabsf(edge)) : 0.0f;
                 edge -= tol;
-                int n = 0;
+                int count = 0;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) n += key[i] >= edge;
-                int at = n;
-#pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const int y = __shfl_up_sync(kFull, at, o);
-                    if (lane >= o) at += y;
-                }
-                found = __shfl_sync(kFull, at, 31);
-                at -= n;
+                for (int i = 0; i < EPL; ++i) count += key[i] >= edge;
+                // places in any order: what is equal is ordered by its index below
+                if (lane == 0) s_found[warp] = 0;
+                s_key[warp][lane] = -INFINITY;
+                __syncwarp();
+                int at = count ? atomicAdd(&s_found[warp], count) : 0;
+                __syncwarp();
+                found = s_found[warp];
                 if (found <= 32) {
-                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < EPL; ++i)
                         if (key[i] >= edge) {
                             s_key[warp][at] = key[i];
+                            s_logit[warp][at] = x[i];
                             s_id[warp][at++] = e0 + i;
                         }
                     __syncwarp();
-                    const float mine = lane < found ? s_key[warp][lane] : -INFINITY;
+                    // keys above this lane's own beyond doubt, and those not below it beyond doubt
+                    mine = s_key[warp][lane];
+                    const float above = mine + tol, below = mine - tol;
                     id = lane < found ? s_id[warp][lane] : 0;
+                    l = s_logit[warp][lane];
                     rank = 0;
-                    bool near = false;
-                    for (int c = 0; c < found; ++c) {
-                        const float o = s_key[warp][c];
-                        rank += o > mine || (o == mine && c < lane);
-                        near |= fabsf(o - mine) <= tol && c != lane;
+                    int not_below = -1;
+                    for (int c = 0; c < found; c += 4) {
+                        const float4 o = *reinterpret_cast<const float4*>(&s_key[warp][c]);
+                        rank += (o.x > above) + (o.y > above) + (o.z > above) + (o.w > above);
+                        not_below += (o.x >= below) + (o.y >= below) + (o.z >= below) + (o.w >= below);
                     }
-                    if (lane >= found) rank = 32;
-                    if (a.bias && __any_sync(kFull, near && lane < found)) {
-                        // equal logits with equal biases are equal in float64 too
-                        const float l = as_float(row[id]), b = __ldg(a.bias + id);
-                        near = false;
-                        for (int c = 0; c < found; ++c) {
-                            const float o = s_key[warp][c], ol = __shfl_sync(kFull, l, c), ob = __shfl_sync(kFull, b, c);
-                            near |= fabsf(o - mine) <= tol && !(l == ol && b == ob);
-                        }
-                        exact = __any_sync(kFull, near && lane < found);
-                    }
+                    unclear = lane < found && rank != not_below;
                 }
             }
         }
         if (!exact && (found == 0 || found > 32)) {
-            // k times the largest key, of the lowest lane that has it
-            float won = 0.0f;
+            // the largest key, of the lowest lane that has it, k times and then while float32 could be wrong about it
             rank = lane;
-            for (int j = 0; j < a.k && !exact; ++j) {
+            found = 0;
+            float edge = -INFINITY, tol = 0.0f;
+            while (true) {
                 const float best = warp_top(top);
+                if (found >= a.k && !(best >= edge)) break;
+                if (best == -INFINITY || found == 32) {
+                    exact = true;
+                    break;
+                }
                 const int src = __ffs(__ballot_sync(kFull, top == best)) - 1;
-                exact = best == -INFINITY;
                 int at = 0;
                 if (lane == src) {
                     top = -INFINITY;
@@ -450,35 +532,32 @@ __global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
                         top = fmaxf(top, key[i]);
                     }
                 }
-                at = __shfl_sync(kFull, at, src & 31);
-                if (lane == j) {
+                at = __shfl_sync(kFull, at, src);
+                if (lane == found) {
                     id = at;
-                    won = best;
+                    mine = best;
+                }
+                if (a.bias) tol = fmaxf(tol, 2.0f * err + 0x1p-22f * fabsf(best));
+                if (++found == a.k) {
+                    if (!a.bias) break;
+                    edge = best - tol;
                 }
             }
-            if (a.bias && !exact) {
-                // neighbours in the order that float32 cannot tell apart
-                const float l = lane < a.k ? as_float(row[id]) : 0.0f, b = lane < a.k ? __ldg(a.bias + id) : 0.0f;
-                const float pw = __shfl_up_sync(kFull, won, 1), pl = __shfl_up_sync(kFull, l, 1),
-                            pb = __shfl_up_sync(kFull, b, 1);
-                bool near = false;
-                if (lane > 0 && lane < a.k && !(l == pl && b == pb)) near = pw - won <= 2.0f * err + 0x1p-22f * fabsf(pw);
-                // and what is left against the last one chosen
-                const float lw = __shfl_sync(kFull, won, a.k - 1), ll = __shfl_sync(kFull, l, a.k - 1),
-                            lb = __shfl_sync(kFull, b, a.k - 1);
-                const float edge = lw - (2.0f * err + 0x1p-22f * fabsf(lw));
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (key[i] >= edge && !(x[i] == ll && __ldg(a.bias + e0 + i) == lb)) near = true;
-                exact = __any_sync(kFull, near);
-            }
+            const float before = __shfl_up_sync(kFull, mine, 1);
+            unclear = a.bias && lane > 0 && lane < found && before - mine <= tol;
+            l = as_float(row[id]);
         }
+        if (!exact && __any_sync(kFull, unclear)) {
+            rank = rank_exact<T>(a, row, e0, n, (double)m, id, found);
+        }
+        if (lane >= found) rank = 32;
         if (exact) {
             id = select_exact<T>(a, row, lane);
+            l = as_float(row[id]);
             rank = lane;
         }
         const bool chosen = rank < a.k;
-        const float l = chosen ? as_float(row[id]) : -INFINITY;
+        if (!chosen) l = -INFINITY;
         // weights: of the chosen logits alone where their sum divides them
         float s = 0.0f;
         if (a.renorm) {
@@ -486,10 +565,10 @@ __global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
             if (chosen && l != -INFINITY) {
                 if (softmax) s = expf(l - lm);
                 // both factors of e^-lm where the scores may be tiny
-                else s = lm < 0.0f ? expf(l - lm) / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));
+                else s = lm < 0.0f ? __fdividef(expf(l - lm), 1.0f + expf(l)) : __fdividef(1.0f, 1.0f + expf(-l));
             }
             const float sum = warp_sum(s);
-            s = sum == 0.0f ? 0.0f : a.scale * (s / sum);
+            s = sum == 0.0f ? 0.0f : a.scale * __fdividef(s, sum);
         } else if (chosen) {
             s = a.scale * (softmax ? (l == -INFINITY ? 0.0f : expf(l - m) * inv) : 1.0f / (1.0f + expf(-l)));
         }
@@ -502,26 +581,41 @@ __global__ void __launch_bounds__(32 * kSelWarps) k_select(const SelectArgs a) {
 
 template <typename T, int EPL>
 cudaError_t launch_select(const SelectArgs& a, int sms, cudaStream_t st) {
-    const int64_t want = ((int64_t)a.T + kSelWarps - 1) / kSelWarps, most = (int64_t)sms * 16;
+    const int64_t want = ((int64_t)a.T + kSelWarps - 1) / kSelWarps, most = (int64_t)sms * 8;
     return launch_pdl(k_select<T, EPL>, dim3((unsigned)(want < most ? want : most)), dim3(32 * kSelWarps), 0, st, a);
 }
 
 template <typename T>
-cudaError_t launch_select_t(const SelectArgs& a, int sms, cudaStream_t st) {
-    if (a.E <= 32) return launch_select<T, 1>(a, sms, st);
-    if (a.E <= 64) return launch_select<T, 2>(a, sms, st);
-    if (a.E <= 128) return launch_select<T, 4>(a, sms, st);
-    if (a.E <= 256) return launch_select<T, 8>(a, sms, st);
-    if (a.E <= 512) return launch_select<T, 16>(a, sms, st);
-    return launch_select<T, 32>(a, sms, st);
+cudaError_t launch_select_t(const SelectArgs& a, int epl, int sms, cudaStream_t st) {
+    switch (epl) {
+        case 1: return launch_select<T, 1>(a, sms, st);
+        case 2: return launch_select<T, 2>(a, sms, st);
+        case 4: return launch_select<T, 4>(a, sms, st);
+        case 8: return launch_select<T, 8>(a, sms, st);
+        case 16: return launch_select<T, 16>(a, sms, st);
+        case 32: return launch_select<T, 32>(a, sms, st);
+        default: return launch_select<T, 64>(a, sms, st);
+    }
 }
 
-// A lane's EPL values are one aligned run of 16-byte pieces inside the row.
-bool wide_rows(const void* logits, int32_t type, int64_t ld, int T, int E) {
-    int epl = 1;
-    while (32 * epl < E) epl *= 2;
-    const int sz = type_bytes(type);
-    return (epl * sz) % 16 == 0 && E % epl == 0 && aligned(logits, 16) && (T == 1 || (ld * sz) % 16 == 0);
+// Experts a lane has when `groups` groups of gs get `lanes` lanes each, a power of
+// two: the fewest that fit the warp (at most 64: E <= 1024, and at least 16 lanes
+// are in use).
+int experts_per_lane(int groups, int gs, int* lanes) {
+    for (int epl = 1;; epl *= 2) {
+        int n = 1;
+        while (n * epl < gs) n *= 2;
+        if (n * groups <= 32) {
+            *lanes = n;
+            return epl;
+        }
+    }
+}
+
+// Whether every lane's run starts at a multiple of its pieces of up to 16 bytes.
+bool wide_rows(const void* logits, int32_t type, int64_t ld, int T, int groups, int gs, int epl) {
+    const int sz = type_bytes(type), piece = epl * sz < 16 ? epl * sz : 16;
+    return aligned(logits, (size_t)piece) && (T == 1 || (ld * sz) % piece == 0) && (groups == 1 || (gs * sz) % piece == 0);
 }
 
 // ---- importances ----------------------------------------------------------
@@ -544,31 +638,49 @@ __global__ void __launch_bounds__(32 * kImpWarps) k_importance(const ImportanceA
     griddep_launch_dependents();
     extern __shared__ float s_sum[];  // [warps][32 EPL]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = max(0, min(EPL, a.E - lane * EPL));
     float acc[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-    for (int t = blockIdx.x * kImpWarps + warp; t < a.T; t += gridDim.x * kImpWarps) {
-        float x[EPL];
-        load_row<T, EPL>(static_cast<const T*>(a.logits) + (size_t)t * a.ld, a.E, a.wide, lane, x);
-        if (a.score == MPE_SCORE_SIGMOID) {
+    constexpr int kRows = EPL <= 8 ? 2 : 1;  // rows in flight together
+    const int step = (int)gridDim.x * kImpWarps;
+    for (int64_t t = blockIdx.x * kImpWarps + warp; t < a.T; t += kRows * step) {
+        float x[kRows][EPL];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) acc[i] += __fdividef(1.0f, 1.0f + __expf(-x[i]));
+        for (int r = 0; r < kRows; ++r)
+            load_row<T, EPL>(static_cast<const T*>(a.logits) + (size_t)(t + r * step) * a.ld + lane * EPL,
+                             t + r * step < a.T ? n : 0, a.wide, x[r]);
+        if (a.score == MPE_SCORE_SIGMOID) {  // of the -inf past the end: 0
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) acc[i] += fast_sigmoid(x[r][i]);
         } else {
-            float m = x[0];
+            float m[kRows], sum[kRows];
 #pragma unroll
-            for (int i = 1; i < EPL; ++i) m = fmaxf(m, x[i]);
-            m = warp_top(m);
-            if (m == -INFINITY) m = 0.0f;  // nothing but -inf: scores of 0 (and NaN stays NaN)
-            float sum = 0.0f;
+            for (int r = 0; r < kRows; ++r) {
+                m[r] = x[r][0];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                x[i] = __expf(x[i] - m);
-                sum += x[i];
+                for (int i = 1; i < EPL; ++i) m[r] = fmaxf(m[r], x[r][i]);
+                m[r] = warp_top(m[r]);
+                if (m[r] == -INFINITY) m[r] = 0.0f;  // nothing but -inf: scores of 0 (and NaN stays NaN)
+                sum[r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    x[r][i] = __expf(x[r][i] - m[r]);
+                    sum[r] += x[r][i];
+                }
             }
-            sum = warp_sum(sum);
-            const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
+            for (int o = 16; o; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) sum[r] += __shfl_xor_sync(kFull, sum[r], o);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float inv = sum[r] == 0.0f ? 0.0f : fast_rcp(sum[r]);
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) acc[i] = fmaf(x[r][i], inv, acc[i]);
+            }
         }
     }
 #pragma unroll
@@ -600,10 +712,12 @@ __global__ void __launch_bounds__(1024) k_importance_join(const float* part, int
     if (lane == 0 && blockIdx.x * 32 + warp < E) out[blockIdx.x * 32 + warp] = (float)(s / T);
 }
 
-// CTAs, each with sums of its own: two to an SM, and more where a warp would
+// CTAs, each with sums of its own: one for a few tokens (a second launch costs
+// more than 16 tokens a warp do), else two to an SM, and more where a warp would
 // add up over 256 rows in float32.
 int importance_parts(int T) {
     const int most = 296, rows = 256 * kImpWarps;
+    if (T <= 16 * kImpWarps) return 1;
     const int n = (int)(((int64_t)T + kImpWarps - 1) / kImpWarps);
     const int long_run = (int)(((int64_t)T + rows - 1) / rows);
     return n < most ? n : (long_run > most ? long_run : most);
@@ -619,13 +733,15 @@ cudaError_t launch_importance(const ImportanceArgs& a, int parts, cudaStream_t s
 }
 
 template <typename T>
-cudaError_t launch_importance_t(const ImportanceArgs& a, int parts, cudaStream_t st) {
-    if (a.E <= 32) return launch_importance<T, 1>(a, parts, st);
-    if (a.E <= 64) return launch_importance<T, 2>(a, parts, st);
-    if (a.E <= 128) return launch_importance<T, 4>(a, parts, st);
-    if (a.E <= 256) return launch_importance<T, 8>(a, parts, st);
-    if (a.E <= 512) return launch_importance<T, 16>(a, parts, st);
-    return launch_importance<T, 32>(a, parts, st);
+cudaError_t launch_importance_t(const ImportanceArgs& a, int epl, int parts, cudaStream_t st) {
+    switch (epl) {
+        case 1: return launch_importance<T, 1>(a, parts, st);
+        case 2: return launch_importance<T, 2>(a, parts, st);
+        case 4: return launch_importance<T, 4>(a, parts, st);
+        case 8: return launch_importance<T, 8>(a, parts, st);
+        case 16: return launch_importance<T, 16>(a, parts, st);
+        default: return launch_importance<T, 32>(a, parts, st);
+    }
 }
 
 // Checks that both calls share; 0 or an error code.
@@ -637,7 +753,7 @@ int check_logits(const char* who, const void* logits, int32_t type, int64_t ld, 
         return report_global_errorf(MPE_ERR_INVALID, "%s: bad score %d", who, score);
     if (type != MPE_TYPE_F32 && type != MPE_TYPE_BF16 && type != MPE_TYPE_F16)
         return report_global_errorf(MPE_ERR_INVALID, "%s: bad type %d", who, type);
-    if (ld < E || ld >= (int64_t)1 << 38)
+    if (T > 1 && (ld < E || ld >= (int64_t)1 << 38))
         return report_global_errorf(MPE_ERR_INVALID, "%s: ld=%lld for %d experts", who, (long long)ld, E);
     if (T > 0 && !logits) return report_global_errorf(MPE_ERR_INVALID, "%s: null logits", who);
     if (!aligned(logits, (size_t)type_bytes(type)))
@@ -656,40 +772,49 @@ int launched(const char* who, cudaError_t e) {
 
 using namespace mpe;
 
-extern "C" int mpe_select_experts(const mpe_select_config* cfg, const void* logits, int32_t type,
-                                  int64_t ld, int32_t T, const float* bias, int32_t* ids, float* w,
-                                  void* stream) {
+extern "C" int mpe_select_experts(const mpe_select_args* p, void* stream) {
     constexpr const char* who = "mpe_select_experts";
-    if (!cfg) return report_global_error(MPE_ERR_INVALID, "mpe_select_experts: null config");
-    if (T < 0) return report_global_errorf(MPE_ERR_INVALID, "%s: T=%d", who, T);
-    const int rc = check_logits(who, logits, type, ld, T, cfg->E, cfg->score);
+    if (!p) return report_global_errorf(MPE_ERR_INVALID, "%s: null args", who);
+    if (p->T < 0) return report_global_errorf(MPE_ERR_INVALID, "%s: T=%d", who, p->T);
+    const int rc = check_logits(who, p->logits, p->type, p->ld, p->T, p->E, p->score);
     if (rc != MPE_OK) return rc;
-    if (cfg->n_groups < 1 || cfg->n_groups > MPE_MAX_GROUPS || cfg->E % cfg->n_groups)
+    if (p->n_groups < 1 || p->n_groups > MPE_MAX_GROUPS || p->E % p->n_groups)
         return report_global_errorf(MPE_ERR_INVALID, "%s: n_groups=%d (1 .. %d, a divisor of E=%d)", who,
-                                    cfg->n_groups, MPE_MAX_GROUPS, cfg->E);
-    if (cfg->keep_groups < 1 || cfg->keep_groups > cfg->n_groups)
-        return report_global_errorf(MPE_ERR_INVALID, "%s: keep_groups=%d of %d", who, cfg->keep_groups,
-                                    cfg->n_groups);
-    if (cfg->group_score != MPE_GROUP_MAX && cfg->group_score != MPE_GROUP_TOP2)
-        return report_global_errorf(MPE_ERR_INVALID, "%s: bad group_score %d", who, cfg->group_score);
-    if (cfg->k < 1 || cfg->k > MPE_MAX_TOPK || cfg->k > cfg->keep_groups * (cfg->E / cfg->n_groups))
-        return report_global_errorf(MPE_ERR_INVALID, "%s: k=%d (1 .. %d, at most the %d experts kept)", who,
-                                    cfg->k, MPE_MAX_TOPK, cfg->keep_groups * (cfg->E / cfg->n_groups));
-    if ((int64_t)T * cfg->k > MPE_MAX_ASSIGNMENTS)
-        return report_global_errorf(MPE_ERR_INVALID, "%s: T*k=%lld above %d", who,
-                                    (long long)T * cfg->k, MPE_MAX_ASSIGNMENTS);
-    if (T == 0) return MPE_OK;
-    if (!ids || !w) return report_global_errorf(MPE_ERR_INVALID, "%s: null output", who);
-    if (!aligned(ids, 4) || !aligned(w, 4) || !aligned(bias, 4))
+                                    p->n_groups, MPE_MAX_GROUPS, p->E);
+    if (p->keep_groups < 1 || p->keep_groups > p->n_groups)
+        return report_global_errorf(MPE_ERR_INVALID, "%s: keep_groups=%d of %d", who, p->keep_groups, p->n_groups);
+    if (p->group_score != MPE_GROUP_MAX && p->group_score != MPE_GROUP_TOP2)
+        return report_global_errorf(MPE_ERR_INVALID, "%s: bad group_score %d", who, p->group_score);
+    const int open = p->keep_groups * (p->E / p->n_groups);
+    if (p->k < 1 || p->k > MPE_MAX_TOPK || p->k > open)
+        return report_global_errorf(MPE_ERR_INVALID, "%s: k=%d (1 .. %d, at most the %d experts kept)", who, p->k,
+                                    MPE_MAX_TOPK, open);
+    if ((int64_t)p->T * p->k > MPE_MAX_ASSIGNMENTS)
+        return report_global_errorf(MPE_ERR_INVALID, "%s: T*k=%lld above %d", who, (long long)p->T * p->k,
+                                    MPE_MAX_ASSIGNMENTS);
+    if (p->T == 0) return MPE_OK;
+    if (!p->ids || !p->w) return report_global_errorf(MPE_ERR_INVALID, "%s: null output", who);
+    if (!aligned(p->ids, 4) || !aligned(p->w, 4) || !aligned(p->bias, 4))
         return report_global_errorf(MPE_ERR_INVALID, "%s: ids, w or bias not aligned to 4 bytes", who);
-    SelectArgs a{logits, ld, bias, ids, w, T, cfg->E, cfg->k, cfg->score, cfg->n_groups, cfg->keep_groups,
-                 cfg->group_score, cfg->renormalize != 0, cfg->scale, wide_rows(logits, type, ld, T, cfg->E)};
+    const Block ids(p->ids, 1, (int64_t)p->T * p->k, 0, 4), w(p->w, 1, (int64_t)p->T * p->k, 0, 4);
+    const Block logits(p->logits, p->T, p->E, p->ld, type_bytes(p->type));
+    auto over_input = [&](const Block& b) {
+        return overlap(b, logits) || (p->bias && overlap(b, Block(p->bias, 1, p->E, 0, 4)));
+    };
+    if (overlap(ids, w) || over_input(ids) || over_input(w))
+        return report_global_errorf(MPE_ERR_INVALID, "%s: ids or w overlaps another argument", who);
+    const int groups = p->keep_groups < p->n_groups ? p->n_groups : 1, gs = p->E / groups;
+    int lanes = 1;
+    const int epl = experts_per_lane(groups, gs, &lanes);
+    const SelectArgs a{p->logits, p->ld, p->bias, p->ids, p->w, p->T, p->E, p->k, p->score, p->n_groups,
+                       p->keep_groups, p->group_score, p->renormalize != 0, p->scale, lanes,
+                       wide_rows(p->logits, p->type, p->ld, p->T, groups, gs, epl)};
     const int sms = current_sm_count();
     if (sms <= 0) return report_global_errorf(MPE_ERR_CUDA, "%s: no current device", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return launched(who, type == MPE_TYPE_F32    ? launch_select_t<float>(a, sms, st)
-                         : type == MPE_TYPE_BF16 ? launch_select_t<__nv_bfloat16>(a, sms, st)
-                                                 : launch_select_t<__half>(a, sms, st));
+    return launched(who, p->type == MPE_TYPE_F32    ? launch_select_t<float>(a, epl, sms, st)
+                         : p->type == MPE_TYPE_BF16 ? launch_select_t<__nv_bfloat16>(a, epl, sms, st)
+                                                    : launch_select_t<__half>(a, epl, sms, st));
 }
 
 extern "C" size_t mpe_expert_importance_workspace(int32_t T, int32_t E) {
@@ -698,28 +823,32 @@ extern "C" size_t mpe_expert_importance_workspace(int32_t T, int32_t E) {
     return parts > 1 ? (size_t)parts * E * sizeof(float) : 0;
 }
 
-extern "C" int mpe_expert_importance(const void* logits, int32_t type, int64_t ld, int32_t T, int32_t E,
-                                     int32_t score, float* p_out, void* workspace, size_t workspace_bytes,
-                                     void* stream) {
+extern "C" int mpe_expert_importance(const mpe_importance_args* p, void* stream) {
     constexpr const char* who = "mpe_expert_importance";
-    if (T < 1) return report_global_errorf(MPE_ERR_INVALID, "%s: T=%d", who, T);
-    const int rc = check_logits(who, logits, type, ld, T, E, score);
+    if (!p) return report_global_errorf(MPE_ERR_INVALID, "%s: null args", who);
+    if (p->T < 1) return report_global_errorf(MPE_ERR_INVALID, "%s: T=%d", who, p->T);
+    const int rc = check_logits(who, p->logits, p->type, p->ld, p->T, p->E, p->score);
     if (rc != MPE_OK) return rc;
-    if (!p_out || !aligned(p_out, 4))
+    if (!p->p_out || !aligned(p->p_out, 4))
         return report_global_errorf(MPE_ERR_INVALID, "%s: p_out null or not aligned to 4 bytes", who);
-    const size_t need = mpe_expert_importance_workspace(T, E);
-    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
-        return report_global_errorf(MPE_ERR_INVALID, "%s: the workspace needs %zu bytes, 16-byte aligned", who,
-                                    need);
-    const int parts = importance_parts(T);
-    ImportanceArgs a{logits, ld, parts > 1 ? nullptr : p_out, static_cast<float*>(workspace), T, E, score,
-                     wide_rows(logits, type, ld, T, E)};
+    const size_t need = mpe_expert_importance_workspace(p->T, p->E);
+    if (need && (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 16)))
+        return report_global_errorf(MPE_ERR_INVALID, "%s: the workspace needs %zu bytes, 16-byte aligned", who, need);
+    const Block out(p->p_out, 1, p->E, 0, 4), logits(p->logits, p->T, p->E, p->ld, type_bytes(p->type));
+    const Block ws(p->workspace, 1, (int64_t)need, 0, 1);
+    if (overlap(out, logits) || (need && (overlap(ws, logits) || overlap(ws, out))))
+        return report_global_errorf(MPE_ERR_INVALID, "%s: p_out or the workspace overlaps another argument", who);
+    const int parts = importance_parts(p->T);
+    int lanes = 1;
+    const int epl = experts_per_lane(1, p->E, &lanes);
+    const ImportanceArgs a{p->logits, p->ld, parts > 1 ? nullptr : p->p_out, static_cast<float*>(p->workspace), p->T,
+                           p->E, p->score, wide_rows(p->logits, p->type, p->ld, p->T, 1, p->E, epl)};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = type == MPE_TYPE_F32    ? launch_importance_t<float>(a, parts, st)
-                    : type == MPE_TYPE_BF16 ? launch_importance_t<__nv_bfloat16>(a, parts, st)
-                                            : launch_importance_t<__half>(a, parts, st);
+    cudaError_t e = p->type == MPE_TYPE_F32    ? launch_importance_t<float>(a, epl, parts, st)
+                    : p->type == MPE_TYPE_BF16 ? launch_importance_t<__nv_bfloat16>(a, epl, parts, st)
+                                               : launch_importance_t<__half>(a, epl, parts, st);
     if (e == cudaSuccess && parts > 1)
-        e = launch_pdl(k_importance_join, dim3((E + 31) / 32), dim3(1024), 0, st, (const float*)a.part, parts, E,
-                       T, p_out);
+        e = launch_pdl(k_importance_join, dim3((p->E + 31) / 32), dim3(1024), 0, st, (const float*)a.part, parts,
+                       p->E, p->T, p->p_out);
     return launched(who, e);
 }

@@ -92,3 +92,37 @@ def test_repage_from_importances(layer):
     assert int(after.astype(np.int64).sum()) <= 4 * wl.E
     ctx.repage(wl.budget_bits, p)
     assert ctx.bits().shape == before.shape and ctx.status() == 0
+
+
+def test_binding_checks():
+    import mixed_precision_expert_b200 as mpe
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device="cuda")
+    l = z(4, 64)
+    bad = [lambda: mpe.select_experts(l.double(), 4), lambda: mpe.select_experts(z(64, 4).t(), 4),
+           lambda: mpe.select_experts(l[0], 4), lambda: mpe.select_experts(l, 4, bias=z(63)),
+           lambda: mpe.select_experts(l, 4, bias=z(64).half()), lambda: mpe.select_experts(l, 4, bias=z(128)[::2]),
+           lambda: mpe.select_experts(l, 4, bias=torch.zeros(64)), lambda: mpe.select_experts(l, 4, ids=z(4, 4)),
+           lambda: mpe.select_experts(l, 4, w=z(4, 5)), lambda: mpe.select_experts(l, 4, w=z(4, 8)[:, ::2]),
+           lambda: mpe.select_experts(l, 4, w=z(4, 4).half()), lambda: mpe.expert_importance(l.int()),
+           lambda: mpe.expert_importance(l, out=z(64).double()), lambda: mpe.expert_importance(l, out=z(63))]
+    bf = torch.bfloat16
+    x, w = z(4, 64, dt=bf), z(128, 64, dt=bf)
+    for kw in (dict(x=x.half()), dict(x=x[:, :32]), dict(x=z(64, 4, dt=bf).t()), dict(weight=w[:, :32]),
+               dict(weight=w.cpu()), dict(weight=w[:127], gated=True), dict(bias=z(64)), dict(bias=z(128).half()),
+               dict(out=z(4, 127)), dict(out=z(4, 128), out_dtype=bf), dict(residual=z(4, 128), out_dtype=bf),
+               dict(residual=z(5, 128)), dict(out=z(4, 128).double()), dict(residual=z(4, 128, dt=bf)[0])):
+        bad.append(lambda kw=kw: mpe.linear(**{"x": x, "weight": w, **kw}))
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    # what the library itself refuses
+    wide = z(6, 72, dt=bf)
+    for call in (lambda: mpe.select_experts(l, 65), lambda: mpe.select_experts(l, 4, n_groups=3),
+                 lambda: mpe.linear(x.float(), w.float()), lambda: mpe.linear(wide[:4, 1:65], w),
+                 lambda: mpe.linear(z(6, 68, dt=bf)[:4, :64], w), lambda: mpe.linear(x, w, out=w[:8].view(4, 128)),
+                 lambda: mpe.linear(x, w, act=9)):
+        with pytest.raises(mpe.MpeError) as e:
+            call()
+        assert e.value.code == -1
+    assert mpe.select_experts(l[:0], 4)[0].shape == (0, 4)
+    assert mpe.linear(x[:0], w).shape == (0, 128)

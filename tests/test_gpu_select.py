@@ -80,7 +80,8 @@ def test_token_counts(mpe, T):
 
 
 @pytest.mark.parametrize("E,G,keep,k", [(256, 8, 4, 8), (256, 8, 1, 8), (160, 8, 3, 6), (64, 32, 5, 7), (96, 3, 2, 32),
-                                        (32, 32, 8, 8), (1024, 32, 4, 8), (512, 16, 15, 9), (60, 4, 2, 4), (30, 10, 7, 5)])
+                                        (32, 32, 8, 8), (1024, 32, 4, 8), (512, 16, 15, 9), (60, 4, 2, 4), (30, 10, 7, 5),
+                                        (1023, 3, 2, 8), (1020, 17, 5, 8), (14, 7, 3, 3), (31, 31, 9, 9), (672, 6, 5, 16)])
 @pytest.mark.parametrize("how", ["max", "top2"])
 def test_groups(mpe, E, G, keep, k, how):
     for score in ("softmax", "sigmoid"):
