@@ -114,27 +114,35 @@ __device__ __forceinline__ void store_run(const Epilogue& e, int m, int n, const
     }
 }
 
-// out[m, n .. n + 3] from the product's sums v (and the up projection's, u).
-template <bool GATED>
-__device__ __forceinline__ void finish(const Epilogue& e, int m, int n, float (&v)[4], float (&u)[4]) {
+// out[m, n .. n + V - 1], V = 4 (whole rows of runs) or 1, from the product's sums v
+// (and the up projection's, u).
+template <int V, bool GATED>
+__device__ __forceinline__ void finish(const Epilogue& e, int m, int n, float (&v)[V], float (&u)[V]) {
     if (n >= e.N) return;
-    float r[4];
-    if (e.residual) load_run(e, e.residual, e.ldr, m, n, r);
+    float r[V];
+    const size_t at = (size_t)m * e.ldo + n, from = (size_t)m * e.ldr + n;
+    if (e.residual) {
+        if constexpr (V == 4) load_run(e, e.residual, e.ldr, m, n, r);
+        else r[0] = load_as_float(e.residual, from, e.out_type);
+    }
     if (e.bias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V; ++i) {
             if (n + i >= e.N) break;
             v[i] += load_as_float(e.bias, n + i, e.bias_type);
             if (GATED) u[i] += load_as_float(e.bias, (size_t)e.N + n + i, e.bias_type);
         }
     }
-    activate<4>(v, e.act);
+    activate<V>(v, e.act);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V; ++i) {
         if (GATED) v[i] *= u[i];
         if (e.residual) v[i] += r[i];
     }
-    store_run(e, m, n, v);
+    if constexpr (V == 4) store_run(e, m, n, v);
+    else if (e.out_type == MPE_TYPE_F32) static_cast<float*>(e.out)[at] = v[0];
+    else if (e.out_type == MPE_TYPE_BF16) static_cast<__nv_bfloat16*>(e.out)[at] = __float2bfloat16_rn(v[0]);
+    else static_cast<__half*>(e.out)[at] = __float2half_rn(v[0]);
 }
 
 // ---------------------------------------------------------------------------
@@ -145,18 +153,25 @@ __device__ __forceinline__ void finish(const Epilogue& e, int m, int n, float (&
 // cluster share K. Each copies its sums of a token to the CTA that finishes it,
 // where they are added up in the order of the ranks: no workspace, and a result
 // that does not depend on timing.
-//   warp 0   loads: per step of 64 inputs a box of w (gated: two) and one of x
-//   warp 1   MMAs, M = 128, N = NT
-//   all      tensor memory -> shared memory, sums, epilogue
+//   warp 0     loads: per step of 64 inputs a box of w (gated: two) and one of x
+//   warp 1     MMAs, M = 128, N = NT
+//   warps 4-7  tensor memory -> shared memory
+//   all        sums over the ranks, epilogue
+// The tensor cores cut what they add to an accumulator instead of rounding it: the
+// error grows by about 10^-9 of the result a value of K, always towards zero
+// (measured: 1.6e-5 at K = 14336). That is nothing beside the rounding of a 16-bit
+// result; for a float32 result the MMAs change between two accumulators every
+// kChain inputs, and warps 4-7 add them up in registers, rounding to nearest.
 // What the next launch can do before this one has ended: its CTAs start where
 // shared memory is left, and bring their weights into L2.
 constexpr int kKStep = 64;
 constexpr int kRows = 128;
+constexpr int kChain = 512;
 constexpr int kAhead = 8;  // steps of w brought into L2 before earlier kernels have ended
 
 template <int NT>
 struct Narrow {
-    static constexpr int kThreads = NT <= 32 ? 128 : 256;
+    static constexpr int kThreads = 256;
     static constexpr int kStageBytes = (kRows + NT) * 128;
     static constexpr int kStages = NT == 128 ? 5 : NT == 64 ? 3 : 4;
     static constexpr int kRing = kStages * kStageBytes;  // then the sums, [token][row]
@@ -165,13 +180,13 @@ struct Narrow {
     // what the other ranks send: [rank][token][row], S ceil(NT / S) tokens
     static constexpr int kSmem = 1024 + kRing + kPart + 256;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-    static constexpr int kCols = NT < 32 ? 32 : NT;
+    static constexpr int kCols = 2 * NT;  // two accumulators
 };
 
 template <int NT, int S, bool GATED>
 __global__ void __launch_bounds__(Narrow<NT>::kThreads)
 k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Epilogue e,
-         const int nk, const uint32_t idesc) {
+         const int nk, const int chain, const uint32_t idesc) {
     using C = Narrow<NT>;
     static_assert(NT % S == 0, "tokens of a rank");
     constexpr int kOut = GATED ? kRows / 2 : kRows;  // outputs of a tile
@@ -182,8 +197,9 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
     float* sent = reinterpret_cast<float*>(ring + C::kRing);
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kRing + C::kPart);
     uint64_t* empty = full + C::kStages;
-    uint64_t* done = empty + C::kStages;
-    uint64_t* got = done + 1;  // the other ranks' sums are here
+    uint64_t* acc_full = empty + C::kStages;  // [2]: a chain's sums are complete
+    uint64_t* acc_empty = acc_full + 2;       // [2]: read by warps 4-7
+    uint64_t* got = acc_empty + 2;            // the other ranks' sums are here
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(got + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
@@ -202,7 +218,10 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        mbar_init(done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
+        }
         mbar_init(got, 1);
         fence_mbar_init();
         if (S > 1) mbar_arrive_expect_tx(got, (uint32_t)((S - 1) * mine * kRows * 4));
@@ -248,9 +267,13 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
             griddep_launch_dependents();
             const uint32_t d = *tmem_slot;
             const uint64_t desc = tc::smem_desc(smem_u32(ring));
-            int s = 0;
+            int s = 0, left = chain, chains = 0;  // left: steps of this chain; chains: complete ones
             uint32_t phase = 0;
             for (int k = k_first; k < k_last; ++k) {
+                if (left == chain && chains >= 2 && !mbar_wait_bounded(&acc_empty[chains & 1], (uint32_t)(chains / 2 - 1) & 1u)) {
+                    ok = false;
+                    break;
+                }
                 if (!mbar_wait_spin(&full[s], phase)) {
                     ok = false;
                     break;
@@ -259,33 +282,57 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
                 const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (kRows * 128 >> 4);
 #pragma unroll
                 for (int i = 0; i < kKStep / 16; ++i)
-                    tc::mma(d, da + 2 * i, db + 2 * i, idesc, k > k_first || i > 0);
+                    tc::mma(d + (uint32_t)((chains & 1) * NT), da + 2 * i, db + 2 * i, idesc, left < chain || i > 0);
                 tc::commit(&empty[s]);
                 if (++s == C::kStages) s = 0, phase ^= 1u;
+                if (--left == 0 || k + 1 == k_last) {
+                    tc::commit(&acc_full[chains & 1]);
+                    left = chain;
+                    ++chains;
+                }
             }
-            tc::commit(done);
         }
         __syncwarp();
     }
-    ok &= mbar_wait_bounded(done, 0);
-    tc::fence_after();
-    ok = __syncthreads_and(ok);
-    // the sums of this share of K in the ring's place: warps w and w + 4 read lanes
-    // 32 (w % 4) .., every second 16 tokens each
-    const uint32_t tbase = *tmem_slot;
-    if (ok) {
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        float* to = part + (warp & 3) * 32 + lane;
-#pragma unroll 1
-        for (int c = (warp >> 2) * 16; c < mt; c += C::kThreads / 8) {
-            uint32_t v[16];
-            tc::tmem_load16(tbase + lanes + (uint32_t)c, v);
-            tc::tmem_wait();
-            tc::tmem_ready(v);
+    // the sums of this share of K: lanes 32 (w % 4) .. of tensor memory, a row a thread
+    if (warp >= 4) {
+        float sum[NT];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) to[(c + i) * kRows] = __uint_as_float(v[i]);
+        for (int i = 0; i < NT; ++i) sum[i] = 0.0f;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int n = (k_last - k_first + chain - 1) / chain;
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[c & 1], (uint32_t)(c / 2) & 1u));
+            if (!ok) break;
+            tc::fence_after();
+            // at most 64 values on their way at a time
+#pragma unroll
+            for (int g = 0; g < NT; g += 64) {
+                if (g >= mt) break;
+                uint32_t v[NT < 64 ? NT / 16 : 4][16];
+#pragma unroll
+                for (int h = 0; h < 4 && 16 * h < NT; ++h) tc::tmem_load16(*tmem_slot + lanes + (uint32_t)((c & 1) * NT + g + 16 * h), v[h]);
+                tc::tmem_wait();
+#pragma unroll
+                for (int h = 0; h < 4 && 16 * h < NT; ++h) {
+                    tc::tmem_ready(v[h]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[g + 16 * h + i] += __uint_as_float(v[h][i]);
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[c & 1]);
         }
+        // every MMA is done: the ring's place is free
+        float* to = part + (warp & 3) * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            if (i < mt) to[i * kRows] = sum[i];
     }
+    ok = __syncthreads_and(ok);
+    const uint32_t tbase = *tmem_slot;
     tc::fence_before();
     if (S > 1) {
         fence_proxy_async_smem();
@@ -309,26 +356,42 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
         tc::fence_after();
         tc::tmem_free(tbase, C::kCols);
     }
-    // this rank's tokens, four neighbouring outputs of one at a time
-    constexpr int kRuns = kOut / 4;
+    // this rank's tokens, four neighbouring outputs of one a thread; one where rows do
+    // not start at runs of four, so that a warp's are next to each other
     const float* own = part + rank * per * kRows;
-    for (int it = threadIdx.x; it < mine * kRuns; it += C::kThreads) {
-        const int t = it / kRuns, r = it % kRuns * 4;
-        float4 v4[S], u4[S];
+    auto sums_at = [&](int s, int t) { return (S == 1 || s == rank ? own : sent + s * per * kRows) + t * kRows; };
+    if (e.vec) {
+        constexpr int kRuns = kOut / 4;
+        for (int it = threadIdx.x; it < mine * kRuns; it += C::kThreads) {
+            const int t = it / kRuns, r = it % kRuns * 4;
+            float4 v4[S], u4[S];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const float* at = (S == 1 || s == rank ? own : sent + s * per * kRows) + t * kRows + r;
-            v4[s] = *reinterpret_cast<const float4*>(at);
-            if (GATED) u4[s] = *reinterpret_cast<const float4*>(at + kOut);
-        }
-        float v[4] = {v4[0].x, v4[0].y, v4[0].z, v4[0].w}, u[4] = {};
-        if (GATED) tc::add4(u, u4[0]);
+            for (int s = 0; s < S; ++s) {
+                const float* at = sums_at(s, t) + r;
+                v4[s] = *reinterpret_cast<const float4*>(at);
+                if (GATED) u4[s] = *reinterpret_cast<const float4*>(at + kOut);
+            }
+            float v[4] = {v4[0].x, v4[0].y, v4[0].z, v4[0].w}, u[4] = {};
+            if (GATED) tc::add4(u, u4[0]);
 #pragma unroll
-        for (int s = 1; s < S; ++s) {
-            tc::add4(v, v4[s]);
-            if (GATED) tc::add4(u, u4[s]);
+            for (int s = 1; s < S; ++s) {
+                tc::add4(v, v4[s]);
+                if (GATED) tc::add4(u, u4[s]);
+            }
+            finish<4, GATED>(e, m0 + rank * per + t, n0 + r, v, u);
         }
-        finish<GATED>(e, m0 + rank * per + t, n0 + r, v, u);
+    } else {
+#pragma unroll 2
+        for (int it = threadIdx.x; it < mine * kOut; it += C::kThreads) {
+            const int t = it / kOut, r = it % kOut;
+            float v[1] = {sums_at(0, t)[r]}, u[1] = {GATED ? sums_at(0, t)[kOut + r] : 0.0f};
+#pragma unroll
+            for (int s = 1; s < S; ++s) {
+                v[0] += sums_at(s, t)[r];
+                if (GATED) u[0] += sums_at(s, t)[kOut + r];
+            }
+            finish<1, GATED>(e, m0 + rank * per + t, n0 + r, v, u);
+        }
     }
     if (S > 1) tc::cluster_wait();  // the other ranks have what this one sent
 }
@@ -422,6 +485,8 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
     uint64_t* empty = full + C::kStages;                              // each CTA: its stage was multiplied
     uint64_t* acc_full = empty + C::kStages;                          // each CTA: [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by both CTAs' epilogue warps
+    // float32 results: chains of kChain inputs, as in k_narrow; others: all of K
+    const int chain = SZ == 4 ? kChain / kKStep : nk;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank();
@@ -490,29 +555,32 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
             const uint64_t desc = tc::smem_desc(smem_u32(ring));
             int s = 0, b = 0;
             uint32_t phase = 0, acc_phase = 0;
-            int64_t done = 0;
-            for (int64_t t = pair; t < tiles && ok; t += pairs, ++done) {
-                if (done >= 2 && !mbar_wait_bounded(&acc_empty[b], acc_phase ^ 1u)) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after();
-                const uint32_t d = tbase + (uint32_t)(b * BN);
-                for (int k = 0; k < nk; ++k) {
-                    if (!mbar_wait_spin(&full[s], phase)) {
+            bool again = false;  // both accumulators have been in use
+            for (int64_t t = pair; t < tiles && ok; t += pairs) {
+                for (int k0 = 0; k0 < nk && ok; k0 += chain) {
+                    if (again && !mbar_wait_bounded(&acc_empty[b], acc_phase ^ 1u)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after();
-                    const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (128 * 128 >> 4);
+                    const uint32_t d = tbase + (uint32_t)(b * BN);
+                    const int k1 = min(nk, k0 + chain);
+                    for (int k = k0; k < k1; ++k) {
+                        if (!mbar_wait_spin(&full[s], phase)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (128 * 128 >> 4);
 #pragma unroll
-                    for (int i = 0; i < kKStep / 16; ++i)
-                        tc::mma_pair(d, da + 2 * i, db + 2 * i, idesc, k > 0 || i > 0);
-                    tc::commit_pair(&empty[s]);
-                    if (++s == C::kStages) s = 0, phase ^= 1u;
+                        for (int i = 0; i < kKStep / 16; ++i)
+                            tc::mma_pair(d, da + 2 * i, db + 2 * i, idesc, k > k0 || i > 0);
+                        tc::commit_pair(&empty[s]);
+                        if (++s == C::kStages) s = 0, phase ^= 1u;
+                    }
+                    tc::commit_pair(&acc_full[b]);
+                    if (++b == 2) b = 0, acc_phase ^= 1u, again = true;
                 }
-                tc::commit_pair(&acc_full[b]);
-                if (++b == 2) b = 0, acc_phase ^= 1u;
             }
         }
         __syncwarp();
@@ -548,12 +616,47 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                     next[i] = *reinterpret_cast<const uint4*>(static_cast<const V*>(e.residual) + rt0 + (size_t)(8 * i) * e.ldr + c);
             };
             if (e.residual && whole(0)) fetch(0);
+            // the chains before the last one: [0, kHalf) of the outputs (the gate's), then the up projection's
+            float sum[SZ == 4 ? BN / 2 : 1];
+            if constexpr (SZ == 4) {
+#pragma unroll
+                for (int i = 0; i < BN / 2; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+                for (int k0 = 0; k0 + chain < nk; k0 += chain) {
+                    if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + half * kHalf);
+#pragma unroll
+                    for (int g = 0; g < BN / 2; g += 32) {
+                        uint32_t v[2][16];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = g + 16 * h;
+                            tc::tmem_load16(acc + (uint32_t)(at < kHalf ? at : kOut + at - kHalf), v[h]);
+                        }
+                        tc::tmem_wait();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            tc::tmem_ready(v[h]);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[g + 16 * h + i] += __uint_as_float(v[h][i]);
+                        }
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::peer_arrive(tc::peer_addr(smem_u32(&acc_empty[b]), 0));
+                    if (++b == 2) b = 0, phase ^= 1u;
+                }
+            }
             if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after();
             const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + half * kHalf);
-#pragma unroll 1  // the activations' code once, not once a chunk
-            for (int c = 0; c < kHalf && ok; c += kChunk) {
+#pragma unroll(SZ == 4 ? kHalf / kChunk : 1)  // 16-bit: the activations' code once; float32: sum[] is registers
+            for (int c = 0; c < kHalf; c += kChunk) {
+                if (!ok) break;
                 if (n0 + c >= e.N || m >= e.M) break;
                 uint32_t v[kChunk / 16][16], u[kChunk / 16][16];
 #pragma unroll
@@ -580,7 +683,10 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 }
                 float f[kChunk];
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) f[i] = __uint_as_float(v[i / 16][i % 16]);
+                for (int i = 0; i < kChunk; ++i) {
+                    f[i] = __uint_as_float(v[i / 16][i % 16]);
+                    if constexpr (SZ == 4) f[i] += sum[c + i];
+                }
                 if (e.bias) {
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) f[i] += bias[c + i];
@@ -588,8 +694,11 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 activate<kChunk>(f, e.act);
                 if (GATED) {
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i)
-                        f[i] *= __uint_as_float(u[i / 16][i % 16]) + (e.bias ? bias[kHalf + c + i] : 0.0f);
+                    for (int i = 0; i < kChunk; ++i) {
+                        float up = __uint_as_float(u[i / 16][i % 16]);
+                        if constexpr (SZ == 4) up += sum[kHalf + c + i];
+                        f[i] *= up + (e.bias ? bias[kHalf + c + i] : 0.0f);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -701,8 +810,9 @@ cudaError_t launch_narrow(const mpe_linear_args& p, const Epilogue& e, cudaStrea
     attr[1].val.clusterDim = {(unsigned)S, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_narrow<NT, S, GATED>, mw, mx, e, (p.K + kKStep - 1) / kKStep,
-                              tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
+    const int nk = (p.K + kKStep - 1) / kKStep;
+    return cudaLaunchKernelEx(&cfg, k_narrow<NT, S, GATED>, mw, mx, e, nk,
+                              p.out_type == MPE_TYPE_F32 ? kChain / kKStep : nk, tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
 }
 
 template <int NT, bool GATED>
@@ -753,11 +863,12 @@ cudaError_t launch_wide(const mpe_linear_args& p, const Epilogue& e, int sms, cu
                               tc::instr_desc(kTileM, BN, p.type == MPE_TYPE_BF16));
 }
 
-template <int BN>
-cudaError_t launch_wide_for(const mpe_linear_args& p, const Epilogue& e, int sms, cudaStream_t st) {
+cudaError_t launch_wide_for(const mpe_linear_args& p, const Epilogue& e, int bn, int sms, cudaStream_t st) {
+    // float32: the sums of earlier chains are registers, which takes the narrower tile
     if (p.out_type == MPE_TYPE_F32)
-        return p.gated ? launch_wide<BN, true, 4>(p, e, sms, st) : launch_wide<BN, false, 4>(p, e, sms, st);
-    return p.gated ? launch_wide<BN, true, 2>(p, e, sms, st) : launch_wide<BN, false, 2>(p, e, sms, st);
+        return p.gated ? launch_wide<128, true, 4>(p, e, sms, st) : launch_wide<128, false, 4>(p, e, sms, st);
+    if (bn == 128) return p.gated ? launch_wide<128, true, 2>(p, e, sms, st) : launch_wide<128, false, 2>(p, e, sms, st);
+    return p.gated ? launch_wide<256, true, 2>(p, e, sms, st) : launch_wide<256, false, 2>(p, e, sms, st);
 }
 
 // The kernel for a product: k_wide<tile> (wide) or k_narrow<tile, split>.
@@ -766,15 +877,56 @@ struct Choice {
     int tile, split;
 };
 
+// The form with the least estimated time, in us, from times measured on B200 over
+// M 1 .. 8192, N 128 .. 14336, K 512 .. 14336:
+//   k_narrow<NT>  starts and ends in 2.4 + 0.047 NT (64 tokens x 128 x 2048, no
+//                 split: 13.4 with NT 32, 14.3 with NT 64); a step takes a CTA
+//                 0.3, or what an SM takes in at 112 GB/s where it has several
+//                 CTAs (128 x 2048 x 2048, NT 64, split 1, 2, 4: 15.4, 10.8, 8.2);
+//                 tiles of tokens that read the same rows of w at once cost 0.06
+//                 each (786 x 48 x 1056: 9.4 with NT 16, 6.9 with 32, 6.3 with 64);
+//                 an SM holds two CTAs (NT 128: one), and a second round starts
+//                 and ends again, mostly hidden (512 x 7168 x 2048: 33 with NT 64
+//                 against 16.9 for k_wide<256>)
+//   k_wide<BN>    starts and ends in 7 (BN 256: 8), 0.28 a step and round of a
+//                 pair of CTAs (1024 x 2048 x 2048: 15.6 with 256, 16.2 with 128,
+//                 18 for k_narrow<64>; 512 x 2048 x 7168: 38, against 28.5 for
+//                 k_narrow<128> with split 2)
+// and all of them the time of memory at 6 TB/s, which hides most of the steps (or
+// is hidden by them).
 Choice choose(const mpe_linear_args& p, int sms) {
-    if (p.M > 128) return {true, 256, 1};
-    const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-    const int per = p.gated ? 64 : 128;
-    const int64_t tiles = (int64_t)((p.N + per - 1) / per) * ((p.M + nt - 1) / nt);
     const int nk = (p.K + kKStep - 1) / kKStep;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * sms && nk >= 4 * split) split *= 2;
-    return {false, nt, split};
+    const int per = p.gated ? kRows / 2 : kRows;
+    const double wrows = p.gated ? 2.0 * p.N : p.N;
+    const double memory =
+        (2.0 * p.K * (p.M + wrows) + (p.residual ? 2.0 : 1.0) * type_bytes(p.out_type) * p.M * p.N) / 6e6;
+    auto both = [&](double steps) { return (steps > memory ? steps : memory) + 0.25 * (steps > memory ? memory : steps); };
+    Choice best{true, 256, 1};
+    double least = 1e30;
+    auto offer = [&](const Choice& c, double us) {
+        if (us < least) best = c, least = us;
+    };
+    for (int bn = 128; bn <= (p.out_type == MPE_TYPE_F32 ? 128 : 256); bn += 128) {
+        const int out = p.gated ? bn / 2 : bn;
+        const double tiles = (double)((p.M + kTileM - 1) / kTileM) * ((p.N + out - 1) / out);
+        const double rounds = (double)(int64_t)((tiles + sms / 2 - 1) / (sms / 2));
+        offer({true, bn, 1}, (bn == 256 ? 8.0 : 7.0) + both(rounds * nk * 0.28));
+    }
+    const int64_t ntiles = (p.N + per - 1) / per;
+    for (int nt = 16; nt <= 128 && nt < 2 * p.M + 16; nt *= 2) {
+        const int64_t mtiles = (p.M + nt - 1) / nt;
+        if (mtiles > 65535) continue;  // the grid's y
+        const double fixed = 2.4 + 0.047 * nt + 0.06 * mtiles, ingest = (kRows + nt) * 128 / 112e3;
+        for (int s = 1; s <= 8 && (s == 1 || nk >= 2 * s); s *= 2) {
+            const double ctas = (double)ntiles * mtiles * s, slots = nt == 128 ? sms : 2 * sms;
+            if (ntiles * s > INT32_MAX) continue;  // the grid's x
+            const double rounds = (double)(int64_t)((ctas + slots - 1) / slots);
+            const double there = (ctas < slots ? ctas : slots) / sms;  // CTAs an SM
+            const double step = there * ingest > 0.3 ? there * ingest : 0.3;
+            offer({false, nt, s}, fixed + 0.7 * fixed * (rounds - 1) + both(rounds * ((nk + s - 1) / s) * step));
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -830,7 +982,7 @@ extern "C" int mpe_linear(const mpe_linear_args* p, void* stream) {
     const int vec = runs(p->out, p->ldo) && (!p->residual || runs(p->residual, p->ldr));
     const Epilogue e{p->bias, p->residual, p->out, p->ldr, p->ldo, p->M, p->N, p->bias_type, p->out_type, p->act, vec};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t err = how.wide   ? (how.tile == 256 ? launch_wide_for<256>(*p, e, sms, st) : launch_wide_for<128>(*p, e, sms, st))
+    const cudaError_t err = how.wide   ? launch_wide_for(*p, e, how.tile, sms, st)
                             : p->gated ? launch_narrow_for<true>(*p, e, how.tile, how.split, st)
                                        : launch_narrow_for<false>(*p, e, how.tile, how.split, st);
     if (err != cudaSuccess) {
