@@ -45,7 +45,7 @@ __device__ __forceinline__ void activate(float (&v)[V], int act) {
             v[i] = __fdividef(v[i], 1.0f + expf(-1.59576912f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
     } else if (act == MPE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678f * v[i]);
+        for (int i = 0; i < V; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(0.70710678f * v[i]));  // erfcf: twice the time
     } else if (act == MPE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
@@ -114,36 +114,50 @@ __device__ __forceinline__ void store_run(const Epilogue& e, int m, int n, const
     }
 }
 
-// out[m, n .. n + V - 1], V = 4 (whole rows of runs) or 1, from the product's sums v
-// (and the up projection's, u).
+// Outputs n .. n + V - 1 of token m, V = 4 (rows of whole runs) or 1, from the
+// product's sums v (and the up projection's, u): what is read for them first, so
+// that several outputs' reads are in flight together, then the rest.
 template <int V, bool GATED>
-__device__ __forceinline__ void finish(const Epilogue& e, int m, int n, float (&v)[V], float (&u)[V]) {
-    if (n >= e.N) return;
-    float r[V];
-    const size_t at = (size_t)m * e.ldo + n, from = (size_t)m * e.ldr + n;
-    if (e.residual) {
-        if constexpr (V == 4) load_run(e, e.residual, e.ldr, m, n, r);
-        else r[0] = load_as_float(e.residual, from, e.out_type);
-    }
-    if (e.bias) {
+struct Output {
+    float v[V], u[V], b[V], bu[V], r[V];
+    int m, n;
+
+    __device__ __forceinline__ void fetch(const Epilogue& e) {
+        if (e.residual && n < e.N) {
+            if constexpr (V == 4) load_run(e, e.residual, e.ldr, m, n, r);
+            else r[0] = load_as_float(e.residual, (size_t)m * e.ldr + n, e.out_type);
+        }
+        if (e.bias) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (n + i >= e.N) break;
-            v[i] += load_as_float(e.bias, n + i, e.bias_type);
-            if (GATED) u[i] += load_as_float(e.bias, (size_t)e.N + n + i, e.bias_type);
+            for (int i = 0; i < V; ++i) {
+                if (n + i >= e.N) break;
+                b[i] = load_as_float(e.bias, n + i, e.bias_type);
+                if (GATED) bu[i] = load_as_float(e.bias, (size_t)e.N + n + i, e.bias_type);
+            }
         }
     }
-    activate<V>(v, e.act);
+    __device__ __forceinline__ void finish(const Epilogue& e) {
+        if (n >= e.N) return;
+        if (e.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (GATED) v[i] *= u[i];
-        if (e.residual) v[i] += r[i];
+            for (int i = 0; i < V; ++i) {
+                v[i] += b[i];
+                if (GATED) u[i] += bu[i];
+            }
+        }
+        activate<V>(v, e.act);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (GATED) v[i] *= u[i];
+            if (e.residual) v[i] += r[i];
+        }
+        const size_t at = (size_t)m * e.ldo + n;
+        if constexpr (V == 4) store_run(e, m, n, v);
+        else if (e.out_type == MPE_TYPE_F32) static_cast<float*>(e.out)[at] = v[0];
+        else if (e.out_type == MPE_TYPE_BF16) static_cast<__nv_bfloat16*>(e.out)[at] = __float2bfloat16_rn(v[0]);
+        else static_cast<__half*>(e.out)[at] = __float2half_rn(v[0]);
     }
-    if constexpr (V == 4) store_run(e, m, n, v);
-    else if (e.out_type == MPE_TYPE_F32) static_cast<float*>(e.out)[at] = v[0];
-    else if (e.out_type == MPE_TYPE_BF16) static_cast<__nv_bfloat16*>(e.out)[at] = __float2bfloat16_rn(v[0]);
-    else static_cast<__half*>(e.out)[at] = __float2half_rn(v[0]);
-}
+};
 
 // ---------------------------------------------------------------------------
 // Few tokens: the weights stream once, their rows are the MMA's M
@@ -359,40 +373,51 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
     // this rank's tokens, four neighbouring outputs of one a thread; one where rows do
     // not start at runs of four, so that a warp's are next to each other
     const float* own = part + rank * per * kRows;
-    auto sums_at = [&](int s, int t) { return (S == 1 || s == rank ? own : sent + s * per * kRows) + t * kRows; };
-    if (e.vec) {
-        constexpr int kRuns = kOut / 4;
-        for (int it = threadIdx.x; it < mine * kRuns; it += C::kThreads) {
-            const int t = it / kRuns, r = it % kRuns * 4;
-            float4 v4[S], u4[S];
+    auto each = [&](auto v_, auto batch_) {
+        constexpr int V = decltype(v_)::value, kBatch = decltype(batch_)::value, kRuns = kOut / V;
+#pragma unroll 1
+        for (int it = threadIdx.x; it < mine * kRuns; it += kBatch * C::kThreads) {
+            Output<V, GATED> o[kBatch];
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const float* at = sums_at(s, t) + r;
-                v4[s] = *reinterpret_cast<const float4*>(at);
-                if (GATED) u4[s] = *reinterpret_cast<const float4*>(at + kOut);
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = it + j * C::kThreads, t = i / kRuns, r = i % kRuns * V;
+                o[j].m = m0 + rank * per + t;
+                o[j].n = i < mine * kRuns ? n0 + r : e.N;
+                if (i < mine * kRuns) o[j].fetch(e);
             }
-            float v[4] = {v4[0].x, v4[0].y, v4[0].z, v4[0].w}, u[4] = {};
-            if (GATED) tc::add4(u, u4[0]);
 #pragma unroll
-            for (int s = 1; s < S; ++s) {
-                tc::add4(v, v4[s]);
-                if (GATED) tc::add4(u, u4[s]);
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = min(it + j * C::kThreads, mine * kRuns - 1), t = i / kRuns, r = i % kRuns * V;
+                float v[S][V], u[S][V];
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const float* at = (S == 1 || s == rank ? own : sent + s * per * kRows) + t * kRows + r;
+                    if constexpr (V == 4) {
+                        *reinterpret_cast<float4*>(v[s]) = *reinterpret_cast<const float4*>(at);
+                        if (GATED) *reinterpret_cast<float4*>(u[s]) = *reinterpret_cast<const float4*>(at + kOut);
+                    } else {
+                        v[s][0] = at[0];
+                        if (GATED) u[s][0] = at[kOut];
+                    }
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < V; ++i2) {
+                    o[j].v[i2] = v[0][i2];
+                    if (GATED) o[j].u[i2] = u[0][i2];
+#pragma unroll
+                    for (int s = 1; s < S; ++s) {
+                        o[j].v[i2] += v[s][i2];
+                        if (GATED) o[j].u[i2] += u[s][i2];
+                    }
+                }
             }
-            finish<4, GATED>(e, m0 + rank * per + t, n0 + r, v, u);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) o[j].finish(e);
         }
-    } else {
-#pragma unroll 2
-        for (int it = threadIdx.x; it < mine * kOut; it += C::kThreads) {
-            const int t = it / kOut, r = it % kOut;
-            float v[1] = {sums_at(0, t)[r]}, u[1] = {GATED ? sums_at(0, t)[kOut + r] : 0.0f};
-#pragma unroll
-            for (int s = 1; s < S; ++s) {
-                v[0] += sums_at(s, t)[r];
-                if (GATED) u[0] += sums_at(s, t)[kOut + r];
-            }
-            finish<1, GATED>(e, m0 + rank * per + t, n0 + r, v, u);
-        }
-    }
+    };
+    // NT 16 has one run a thread
+    if (e.vec) each(std::integral_constant<int, 4>(), std::integral_constant<int, NT <= 16 ? 1 : 2>());
+    else each(std::integral_constant<int, 1>(), std::integral_constant<int, NT <= 16 ? 2 : 4>());
     if (S > 1) tc::cluster_wait();  // the other ranks have what this one sent
 }
 
@@ -445,24 +470,25 @@ __device__ __forceinline__ uint8_t* staged(uint8_t* base, int r, int j) {
 }
 
 // Single values between the staging rows and global rows m .. m + 31, columns
-// n .. (64 bytes' worth), 8 rows at a time, so that loads are in flight together.
+// n .. (64 bytes' worth), 16 rows at a time, so that loads are in flight together.
 template <typename V, bool STORE>
 __device__ __forceinline__ void move_values(uint8_t* stage, void* base, int64_t ld, int m, int n, int M, int N, int lane) {
     constexpr int kPer = 16 / (int)sizeof(V), kCols = 64 / (int)sizeof(V);
     constexpr int kRowsAt = 32 / kCols;  // rows in one pass of the warp: 1 or 2
+    constexpr int kBatch = 16;
     V* g = static_cast<V*>(base);
     const int c = lane % kCols;
 #pragma unroll 1
-    for (int r0 = lane / kCols; r0 < 32; r0 += 8 * kRowsAt) {
-        V v[8];
+    for (int r0 = lane / kCols; r0 < 32; r0 += kBatch * kRowsAt) {
+        V v[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
             const int r = r0 + i * kRowsAt;
             if (STORE) v[i] = reinterpret_cast<const V*>(staged(stage, r, c / kPer))[c % kPer];
             else if (m + r < M && n + c < N) v[i] = g[(size_t)(m + r) * ld + n + c];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
             const int r = r0 + i * kRowsAt;
             if (!STORE) reinterpret_cast<V*>(staged(stage, r, c / kPer))[c % kPer] = v[i];
             else if (m + r < M && n + c < N) g[(size_t)(m + r) * ld + n + c] = v[i];
@@ -615,7 +641,10 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 for (int i = 0; i < 4; ++i)
                     next[i] = *reinterpret_cast<const uint4*>(static_cast<const V*>(e.residual) + rt0 + (size_t)(8 * i) * e.ldr + c);
             };
-            if (e.residual && whole(0)) fetch(0);
+            if (e.residual) {  // the first chunk's before the wait for the products
+                if (whole(0)) fetch(0);
+                else move_values<V, false>(stage, const_cast<void*>(e.residual), e.ldr, m, n0, e.M, e.N, lane);
+            }
             // the chains before the last one: [0, kHalf) of the outputs (the gate's), then the up projection's
             float sum[SZ == 4 ? BN / 2 : 1];
             if constexpr (SZ == 4) {
@@ -670,7 +699,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
 #pragma unroll
                         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staged(stage, row + 8 * i, piece)) = next[i];
                         if (c + kChunk < kHalf && whole(c + kChunk)) fetch(c + kChunk);
-                    } else {
+                    } else if (c > 0) {
                         move_values<V, false>(stage, const_cast<void*>(e.residual), e.ldr, m, n0 + c, e.M, e.N, lane);
                     }
                     __syncwarp();
@@ -885,6 +914,8 @@ struct Choice {
 //                 CTAs (128 x 2048 x 2048, NT 64, split 1, 2, 4: 15.4, 10.8, 8.2);
 //                 tiles of tokens that read the same rows of w at once cost 0.06
 //                 each (786 x 48 x 1056: 9.4 with NT 16, 6.9 with 32, 6.3 with 64);
+//                 rows that do not start at 128 bytes cost every step two lines
+//                 instead of one (333 x 4096 x 2048, NT 64: 17; x 2040: 26);
 //                 an SM holds two CTAs (NT 128: one), and a second round starts
 //                 and ends again, mostly hidden (512 x 7168 x 2048: 33 with NT 64
 //                 against 16.9 for k_wide<256>)
@@ -913,6 +944,7 @@ Choice choose(const mpe_linear_args& p, int sms) {
         offer({true, bn, 1}, (bn == 256 ? 8.0 : 7.0) + both(rounds * nk * 0.28));
     }
     const int64_t ntiles = (p.N + per - 1) / per;
+    const bool lines = (p.N == 1 || p.ldw % 64 == 0) && (p.M == 1 || p.ldx % 64 == 0) && aligned(p.w, 128) && aligned(p.x, 128);
     for (int nt = 16; nt <= 128 && nt < 2 * p.M + 16; nt *= 2) {
         const int64_t mtiles = (p.M + nt - 1) / nt;
         if (mtiles > 65535) continue;  // the grid's y
@@ -922,7 +954,7 @@ Choice choose(const mpe_linear_args& p, int sms) {
             if (ntiles * s > INT32_MAX) continue;  // the grid's x
             const double rounds = (double)(int64_t)((ctas + slots - 1) / slots);
             const double there = (ctas < slots ? ctas : slots) / sms;  // CTAs an SM
-            const double step = there * ingest > 0.3 ? there * ingest : 0.3;
+            const double one = there * ingest > 0.3 ? there * ingest : 0.3, step = lines ? one : 1.7 * one;
             offer({false, nt, s}, fixed + 0.7 * fixed * (rounds - 1) + both(rounds * ((nk + s - 1) / s) * step));
         }
     }
