@@ -330,11 +330,26 @@ __device__ __forceinline__ float fast_rcp(float v) {
     return r;
 }
 
+__device__ __forceinline__ float one_if_greater(float a, float b) {
+    float r;
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float one_if_not_less(float a, float b) {
+    float r;
+    asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float fast_exp2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // 1 / (1 + e^-l)
 __device__ __forceinline__ float fast_sigmoid(float l) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * l));
-    return fast_rcp(1.0f + e);
+    return fast_rcp(1.0f + fast_exp2(-1.44269504f * l));
 }
 
 // The n-th largest of the lanes' values, or less where some are equal (-inf:
@@ -352,7 +367,6 @@ __device__ __forceinline__ float nth_top(float v, int n, float& best) {
 template <typename T, int EPL>
 __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 : 3) k_select(const SelectArgs a) {
     __shared__ __align__(16) float s_key[kSelWarps][32];
-    __shared__ float s_logit[kSelWarps][32];
     __shared__ int s_id[kSelWarps][32], s_found[kSelWarps];
     griddep_wait();
     griddep_launch_dependents();
@@ -409,21 +423,26 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
             sum = warp_sum(sum);
             inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
         }
-        auto score = [&](float l) {
-            if (!softmax) return fast_sigmoid(l);
-            return l == -INFINITY ? 0.0f : expf(l - m) * inv;
-        };
+        auto score = [&](float l) { return softmax ? (l == -INFINITY ? 0.0f : expf(l - m) * inv) : fast_sigmoid(l); };
         // -inf: not to be chosen, by its key or by its group
         float key[EPL];
+        if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            key[i] = x[i];
-            if (a.bias) key[i] = score(x[i]) + (kHold ? held[i] : i < n ? __ldg(a.bias + e0 + i) : -INFINITY);
+            for (int i = 0; i < EPL; ++i)
+                key[i] = score(x[i]) + (kHold ? held[i] : i < n ? __ldg(a.bias + e0 + i) : -INFINITY);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = x[i];
         }
         if (limited) {
             float m1 = -INFINITY, m2 = -INFINITY;
+            if (sums && !a.bias) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) push2(m1, m2, sums && !a.bias && i < n ? score(x[i]) : key[i]);
+                for (int i = 0; i < EPL; ++i) push2(m1, m2, i < n ? score(x[i]) : -INFINITY);
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) push2(m1, m2, key[i]);
+            }
             for (int o = 1; o < a.lanes; o *= 2) {
                 const float o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
                 push2(m1, m2, o1);
@@ -485,7 +504,6 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
                     for (int i = 0; i < EPL; ++i)
                         if (key[i] >= edge) {
                             s_key[warp][at] = key[i];
-                            s_logit[warp][at] = x[i];
                             s_id[warp][at++] = e0 + i;
                         }
                     __syncwarp();
@@ -493,15 +511,18 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
                     mine = s_key[warp][lane];
                     const float above = mine + tol, below = mine - tol;
                     id = lane < found ? s_id[warp][lane] : 0;
-                    l = s_logit[warp][lane];
-                    rank = 0;
-                    int not_below = -1;
+                    l = a.bias ? as_float(row[id]) : mine;
+                    // (the counts as floats: a comparison gives 1.0 or 0.0)
+                    float over = 0.0f, not_under = -1.0f;
                     for (int c = 0; c < found; c += 4) {
                         const float4 o = *reinterpret_cast<const float4*>(&s_key[warp][c]);
-                        rank += (o.x > above) + (o.y > above) + (o.z > above) + (o.w > above);
-                        not_below += (o.x >= below) + (o.y >= below) + (o.z >= below) + (o.w >= below);
+                        over += one_if_greater(o.x, above) + one_if_greater(o.y, above);
+                        over += one_if_greater(o.z, above) + one_if_greater(o.w, above);
+                        not_under += one_if_not_less(o.x, below) + one_if_not_less(o.y, below);
+                        not_under += one_if_not_less(o.z, below) + one_if_not_less(o.w, below);
                     }
-                    unclear = lane < found && rank != not_below;
+                    rank = (int)over;
+                    unclear = lane < found && over != not_under;
                 }
             }
         }
@@ -624,72 +645,122 @@ struct ImportanceArgs {
     int64_t ld;
     float* out;   // [E], or null: this CTA's sums go to part
     float* part;  // [CTAs][E]
-    int T, E, score, wide;
+    int T, E, score, wide;  // wide: rows are whole, aligned pieces of 16 bytes
 };
 
 constexpr int kImpWarps = 16;
 
-// One warp a token, a lane's EPL columns added up in registers over the tokens;
-// then over the CTA's warps, and over the CTAs in k_importance_join, always in
-// the same order. The fast exponential: 2 + 1.2 d ulp for a score of e^-d.
+// One warp a token, its columns added up in registers over the tokens; then over
+// the CTA's warps, and over the CTAs in k_importance_join, always in the same
+// order. Which columns a lane has does not matter: pieces of 16 bytes, the warp's
+// next to each other (single values where rows are not aligned to that). A lane
+// copies its pieces of the rows to come asynchronously into its own part of shared
+// memory, so that enough rows are on their way to keep memory busy while a row's
+// maximum and sum go round the warp. The fast exponential: 2 + 1.2 d ulp for a
+// score of e^-d.
+template <typename T, int EPL>
+struct ImpRing {
+    static constexpr int kRowBytes = 32 * EPL * (int)sizeof(T);
+    static constexpr int kDepth = EPL * (int)sizeof(T) >= 16 ? (kRowBytes <= 1024 ? 4 : 2) : 0;  // rows ahead
+    static constexpr int kBytes = kImpWarps * (kDepth * kRowBytes > 128 * EPL ? kDepth * kRowBytes : 128 * EPL);
+};
+
+// A row's scores added to acc.
+template <int EPL>
+__device__ __forceinline__ void add_scores(float (&x)[EPL], bool sigmoid, float (&acc)[EPL]) {
+    if (sigmoid) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) acc[i] += fast_sigmoid(x[i]);
+        return;
+    }
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, x[i]);
+    m = warp_top(m);
+    if (m == -INFINITY) m = 0.0f;  // nothing but -inf: scores of 0 (and NaN stays NaN)
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        x[i] = fast_exp2(1.44269504f * (x[i] - m));
+        sum += x[i];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum == 0.0f ? 0.0f : fast_rcp(sum);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
+}
+
 template <typename T, int EPL>
 __global__ void __launch_bounds__(32 * kImpWarps) k_importance(const ImportanceArgs a) {
     griddep_wait();
     griddep_launch_dependents();
-    extern __shared__ float s_sum[];  // [warps][32 EPL]
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    float* s_sum = reinterpret_cast<float*>(s_raw);  // [warps][EPL][32], after the rows
+    using R = ImpRing<T, EPL>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = max(0, min(EPL, a.E - lane * EPL));
+    const int step = (int)gridDim.x * kImpWarps;
+    const bool sigmoid = a.score == MPE_SCORE_SIGMOID;
+    const T* logits = static_cast<const T*>(a.logits);
     float acc[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-    constexpr int kRows = EPL <= 8 ? 2 : 1;  // rows in flight together
-    const int step = (int)gridDim.x * kImpWarps;
-    for (int64_t t = blockIdx.x * kImpWarps + warp; t < a.T; t += kRows * step) {
-        float x[kRows][EPL];
+    int64_t t = blockIdx.x * kImpWarps + warp;
+    constexpr bool kPieced = R::kDepth > 0;
+    constexpr int kPer = kPieced ? 16 / (int)sizeof(T) : 1, kPieces = EPL / kPer;
+    const bool pieced = kPieced && a.wide;
+    if (pieced) {
+        constexpr int kDepth = kPieced ? R::kDepth : 1;
+        uint8_t* ring = s_raw + (size_t)warp * kDepth * R::kRowBytes;  // [row][piece][lane]
+        auto fetch = [&](int64_t row, int slot) {
+            if (row < a.T)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            load_row<T, EPL>(static_cast<const T*>(a.logits) + (size_t)(t + r * step) * a.ld + lane * EPL,
-                             t + r * step < a.T ? n : 0, a.wide, x[r]);
-        if (a.score == MPE_SCORE_SIGMOID) {  // of the -inf past the end: 0
+                for (int p = 0; p < kPieces; ++p)
+                    if ((p * 32 + lane) * kPer < a.E)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         smem_u32(ring + slot * R::kRowBytes + (p * 32 + lane) * 16)),
+                                     "l"(logits + (size_t)row * a.ld + (p * 32 + lane) * kPer)
+                                     : "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
+        for (int d = 0; d < kDepth; ++d) fetch(t + (int64_t)d * step, d);
+        for (int slot = 0; t < a.T; t += step) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            float x[EPL];
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) acc[i] += fast_sigmoid(x[r][i]);
-        } else {
-            float m[kRows], sum[kRows];
+            for (int p = 0; p < kPieces; ++p) {
+                T v[kPer];
+                const uint4 w = *reinterpret_cast<const uint4*>(ring + slot * R::kRowBytes + (p * 32 + lane) * 16);
+                memcpy(v, &w, sizeof(v));
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                m[r] = x[r][0];
-#pragma unroll
-                for (int i = 1; i < EPL; ++i) m[r] = fmaxf(m[r], x[r][i]);
-                m[r] = warp_top(m[r]);
-                if (m[r] == -INFINITY) m[r] = 0.0f;  // nothing but -inf: scores of 0 (and NaN stays NaN)
-                sum[r] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    x[r][i] = __expf(x[r][i] - m[r]);
-                    sum[r] += x[r][i];
-                }
+                for (int i = 0; i < kPer; ++i)
+                    x[p * kPer + i] = (p * 32 + lane) * kPer < a.E ? as_float(v[i]) : -INFINITY;
             }
+            fetch(t + (int64_t)kDepth * step, slot);  // this lane has read its part of the slot
+            add_scores<EPL>(x, sigmoid, acc);
+            if (++slot == kDepth) slot = 0;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the sums take the rows' place
+    } else {
+#pragma unroll 2
+        for (; t < a.T; t += step) {
+            float x[EPL];
 #pragma unroll
-            for (int o = 16; o; o >>= 1)
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) sum[r] += __shfl_xor_sync(kFull, sum[r], o);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float inv = sum[r] == 0.0f ? 0.0f : fast_rcp(sum[r]);
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) acc[i] = fmaf(x[r][i], inv, acc[i]);
-            }
+            for (int i = 0; i < EPL; ++i)
+                x[i] = i * 32 + lane < a.E ? as_float(logits[(size_t)t * a.ld + i * 32 + lane]) : -INFINITY;
+            add_scores<EPL>(x, sigmoid, acc);
         }
     }
+    // by column
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s_sum[(warp * EPL + i) * 32 + lane] = acc[i];
+    for (int i = 0; i < EPL; ++i)
+        s_sum[warp * 32 * EPL + (pieced ? (i / kPer * 32 + lane) * kPer + i % kPer : i * 32 + lane)] = acc[i];
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kImpWarps; ++w) s += s_sum[(w * EPL + e % EPL) * 32 + e / EPL];
+        for (int w = 0; w < kImpWarps; ++w) s += s_sum[w * 32 * EPL + e];
         if (a.out) a.out[e] = (float)((double)s / a.T);
         else a.part[(size_t)blockIdx.x * a.E + e] = s;
     }
@@ -725,7 +796,7 @@ int importance_parts(int T) {
 
 template <typename T, int EPL>
 cudaError_t launch_importance(const ImportanceArgs& a, int parts, cudaStream_t st) {
-    const size_t smem = (size_t)kImpWarps * 32 * EPL * sizeof(float);
+    const size_t smem = ImpRing<T, EPL>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(k_importance<T, EPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
@@ -840,9 +911,10 @@ extern "C" int mpe_expert_importance(const mpe_importance_args* p, void* stream)
         return report_global_errorf(MPE_ERR_INVALID, "%s: p_out or the workspace overlaps another argument", who);
     const int parts = importance_parts(p->T);
     int lanes = 1;
-    const int epl = experts_per_lane(1, p->E, &lanes);
+    const int epl = experts_per_lane(1, p->E, &lanes), sz = type_bytes(p->type);
+    const bool pieces = aligned(p->logits, 16) && (p->T == 1 || p->ld * sz % 16 == 0) && p->E * sz % 16 == 0;
     const ImportanceArgs a{p->logits, p->ld, parts > 1 ? nullptr : p->p_out, static_cast<float*>(p->workspace), p->T,
-                           p->E, p->score, wide_rows(p->logits, p->type, p->ld, p->T, 1, p->E, epl)};
+                           p->E, p->score, pieces};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = p->type == MPE_TYPE_F32    ? launch_importance_t<float>(a, epl, parts, st)
                     : p->type == MPE_TYPE_BF16 ? launch_importance_t<__nv_bfloat16>(a, epl, parts, st)
