@@ -168,31 +168,36 @@ struct Output {
 // where they are added up in the order of the ranks: no workspace, and a result
 // that does not depend on timing.
 //   warp 0     loads: per step of 64 inputs a box of w (gated: two) and one of x
-//   warp 1     MMAs, M = 128, N = NT
+//   warps 1, 2 MMAs, M = 128, N = NT: one issuing thread each, every second step,
+//              an accumulator each (a step takes one thread 0.28 us whatever NT and
+//              the number of stages; two overlap: 1 x 128 x 2048 without a split
+//              12.5 -> 7.8 us)
 //   warps 4-7  tensor memory -> shared memory
 //   all        sums over the ranks, epilogue
 // The tensor cores cut what they add to an accumulator instead of rounding it: the
 // error grows by about 10^-9 of the result a value of K, always towards zero
 // (measured: 1.6e-5 at K = 14336). That is nothing beside the rounding of a 16-bit
-// result; for a float32 result the MMAs change between two accumulators every
-// kChain inputs, and warps 4-7 add them up in registers, rounding to nearest.
-// What the next launch can do before this one has ended: its CTAs start where
-// shared memory is left, and bring their weights into L2.
+// result; for a float32 result an accumulator starts again every kChain inputs,
+// and warps 4-7 add the chains up in registers, rounding to nearest.
 constexpr int kKStep = 64;
 constexpr int kRows = 128;
 constexpr int kChain = 512;
-constexpr int kAhead = 8;  // steps of w brought into L2 before earlier kernels have ended
 
 template <int NT>
 struct Narrow {
     static constexpr int kThreads = 256;
     static constexpr int kStageBytes = (kRows + NT) * 128;
-    static constexpr int kStages = NT == 128 ? 5 : NT == 64 ? 3 : 4;
-    static constexpr int kRing = kStages * kStageBytes;  // then the sums, [token][row]
+    static constexpr int kStages = NT == 128 ? 6 : 4;
+    // An issuer takes every second step, and so every second stage: with an odd
+    // number it would come back to a stage that the other one had in between, and
+    // a barrier's parity cannot tell it a phase from the phase before the last.
+    static_assert(kStages % 2 == 0, "stages of an issuer");
+    static constexpr int kRing = kStages * kStageBytes;
+    // in the ring's place after the last step: this rank's sums, [token][row], and
+    // what the other ranks send, [rank][token][row] of S ceil(NT / S) tokens
     static constexpr int kPart = NT * kRows * 4;
-    static_assert(kPart <= kRing, "the sums take the ring's place");
-    // what the other ranks send: [rank][token][row], S ceil(NT / S) tokens
-    static constexpr int kSmem = 1024 + kRing + kPart + 256;
+    static_assert(2 * kPart <= kRing, "the sums take the ring's place");
+    static constexpr int kSmem = 1024 + kRing + 256;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static constexpr int kCols = 2 * NT;  // two accumulators
 };
@@ -208,12 +213,13 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     float* part = reinterpret_cast<float*>(ring);
-    float* sent = reinterpret_cast<float*>(ring + C::kRing);
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kRing + C::kPart);
+    float* sent = reinterpret_cast<float*>(ring + C::kPart);
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kRing);
     uint64_t* empty = full + C::kStages;
-    uint64_t* acc_full = empty + C::kStages;  // [2]: a chain's sums are complete
+    uint64_t* acc_full = empty + C::kStages;  // [2]: the accumulator's chain is complete
     uint64_t* acc_empty = acc_full + 2;       // [2]: read by warps 4-7
-    uint64_t* got = acc_empty + 2;            // the other ranks' sums are here
+    uint64_t* have_tmem = acc_empty + 2;
+    uint64_t* got = have_tmem + 1;            // the other ranks' sums are here
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(got + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
@@ -236,18 +242,12 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 4);
         }
+        mbar_init(have_tmem, 1);
         mbar_init(got, 1);
         fence_mbar_init();
         if (S > 1) mbar_arrive_expect_tx(got, (uint32_t)((S - 1) * mine * kRows * 4));
     }
     __syncthreads();
-    if (S > 1) tc::cluster_arrive();  // this CTA runs, and its barriers are set up
-    // L2 holds what memory holds, whoever writes it later: no need to wait here
-    if (warp == 2 && lane == 0)
-        for (int k = k_first; k < min(k_last, k_first + kAhead); ++k) {
-            tc::prefetch_box(&map_w, kKStep * k, n0);
-            if (GATED) tc::prefetch_box(&map_w, kKStep * k, e.N + n0);
-        }
     griddep_wait();
     bool ok = true;
     if (warp == 0) {
@@ -272,21 +272,32 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
                 }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // tensor memory is taken after the wait for earlier kernels, and the next
-        // kernel may start only when this one has it: neither can block the other
-        tc::tmem_alloc(tmem_slot, C::kCols);
-        __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+        const int x = warp - 1;  // this issuer's accumulator, and which of every two steps it takes
+        if (x == 0) {
+            // tensor memory is taken after the wait for earlier kernels, and the next
+            // kernel may start only when this one has it: neither can block the other
+            tc::tmem_alloc(tmem_slot, C::kCols);
+            __syncwarp();
+            if (lane == 0) {
+                griddep_launch_dependents();
+                mbar_arrive(have_tmem);
+            }
+        }
         if (lane == 0) {
-            griddep_launch_dependents();
-            const uint32_t d = *tmem_slot;
+            ok = mbar_wait_bounded(have_tmem, 0);
+            const uint32_t d = *tmem_slot + (uint32_t)(x * NT);
             const uint64_t desc = tc::smem_desc(smem_u32(ring));
-            int s = 0, left = chain, chains = 0;  // left: steps of this chain; chains: complete ones
-            uint32_t phase = 0;
-            for (int k = k_first; k < k_last; ++k) {
-                if (left == chain && chains >= 2 && !mbar_wait_bounded(&acc_empty[chains & 1], (uint32_t)(chains / 2 - 1) & 1u)) {
-                    ok = false;
-                    break;
+            int s = x, left = chain;  // left: steps of this chain
+            uint32_t phase = 0, acc_phase = 1;
+            for (int k = k_first + x; k < k_last && ok; k += 2) {
+                if (left == 0) {
+                    left = chain;
+                    acc_phase ^= 1u;
+                    if (!mbar_wait_bounded(&acc_empty[x], acc_phase)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 if (!mbar_wait_spin(&full[s], phase)) {
                     ok = false;
@@ -295,15 +306,11 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
                 tc::fence_after();
                 const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (kRows * 128 >> 4);
 #pragma unroll
-                for (int i = 0; i < kKStep / 16; ++i)
-                    tc::mma(d + (uint32_t)((chains & 1) * NT), da + 2 * i, db + 2 * i, idesc, left < chain || i > 0);
+                for (int i = 0; i < kKStep / 16; ++i) tc::mma(d, da + 2 * i, db + 2 * i, idesc, left < chain || i > 0);
                 tc::commit(&empty[s]);
-                if (++s == C::kStages) s = 0, phase ^= 1u;
-                if (--left == 0 || k + 1 == k_last) {
-                    tc::commit(&acc_full[chains & 1]);
-                    left = chain;
-                    ++chains;
-                }
+                s += 2;
+                if (s >= C::kStages) s -= C::kStages, phase ^= 1u;
+                if (--left == 0 || k + 2 >= k_last) tc::commit(&acc_full[x]);
             }
         }
         __syncwarp();
@@ -314,19 +321,22 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
 #pragma unroll
         for (int i = 0; i < NT; ++i) sum[i] = 0.0f;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int n = (k_last - k_first + chain - 1) / chain;
+        const int steps = k_last - k_first, n = ((steps + 1) / 2 + chain - 1) / chain;  // chains of accumulator 0
 #pragma unroll 1
-        for (int c = 0; c < n; ++c) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[c & 1], (uint32_t)(c / 2) & 1u));
+        for (int c = 0; c < 2 * n && ok; ++c) {
+            const int x = c & 1;
+            if (x == 1 && (c >> 1) * chain >= steps / 2) break;  // accumulator 1 may have one fewer
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[x], (uint32_t)(c >> 1) & 1u));
             if (!ok) break;
             tc::fence_after();
+            const uint32_t acc = *tmem_slot + lanes + (uint32_t)(x * NT);
             // at most 64 values on their way at a time
 #pragma unroll
             for (int g = 0; g < NT; g += 64) {
                 if (g >= mt) break;
                 uint32_t v[NT < 64 ? NT / 16 : 4][16];
 #pragma unroll
-                for (int h = 0; h < 4 && 16 * h < NT; ++h) tc::tmem_load16(*tmem_slot + lanes + (uint32_t)((c & 1) * NT + g + 16 * h), v[h]);
+                for (int h = 0; h < 4 && 16 * h < NT; ++h) tc::tmem_load16(acc + (uint32_t)(g + 16 * h), v[h]);
                 tc::tmem_wait();
 #pragma unroll
                 for (int h = 0; h < 4 && 16 * h < NT; ++h) {
@@ -337,7 +347,7 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
             }
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[c & 1]);
+            if (lane == 0) mbar_arrive(&acc_empty[x]);
         }
         // every MMA is done: the ring's place is free
         float* to = part + (warp & 3) * 32 + lane;
@@ -349,9 +359,9 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
     const uint32_t tbase = *tmem_slot;
     tc::fence_before();
     if (S > 1) {
+        // every CTA's ring is free, and its barriers are set up
         fence_proxy_async_smem();
-        __syncthreads();
-        tc::cluster_wait();
+        tc::cluster_sync();
         // one thread a rank: its tokens' sums to it
         if ((int)threadIdx.x < S && (int)threadIdx.x != rank) {
             const int to = threadIdx.x, n = max(0, min(per, mt - to * per));
@@ -950,7 +960,7 @@ Choice choose(const mpe_linear_args& p, int sms) {
         if (mtiles > 65535) continue;  // the grid's y
         const double fixed = 2.4 + 0.047 * nt + 0.06 * mtiles, ingest = (kRows + nt) * 128 / 112e3;
         for (int s = 1; s <= 8 && (s == 1 || nk >= 2 * s); s *= 2) {
-            const double ctas = (double)ntiles * mtiles * s, slots = nt == 128 ? sms : 2 * sms;
+            const double ctas = (double)ntiles * mtiles * s, slots = nt == 128 ? sms : nt == 16 ? 3 * sms : 2 * sms;
             if (ntiles * s > INT32_MAX) continue;  // the grid's x
             const double rounds = (double)(int64_t)((ctas + slots - 1) / slots);
             const double there = (ctas < slots ? ctas : slots) / sms;  // CTAs an SM
