@@ -237,14 +237,16 @@ _SELECT_ARGS = struct.Struct("=4Qq9if")
 _IMPORTANCE_ARGS = struct.Struct("=4Qq4i")
 _LINEAR_ARGS = struct.Struct("=5Q4q8i")
 _ops = None  # see _load_ops
+_torch = None
 
 
 def _load_ops():
     """(torch's types by MPE_TYPE_*, current device, current stream of a device, the three
     calls): the two queries are what torch.cuda.current_device() and current_stream() wrap, at
     a twentieth of their time."""
-    global _ops
+    global _ops, _torch
     import torch
+    _torch = torch
     torch.cuda.current_device()  # initialises CUDA
     L = lib()
     _ops = ({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16},
@@ -305,22 +307,21 @@ def select_experts(logits, k: int, *, bias=None, score: int = SCORE_SOFTMAX, n_g
     added for the choice alone; the choice is limited to the ``keep_groups`` best of
     ``n_groups`` groups of consecutive experts; weights are the chosen scores, divided by
     their sum with ``renormalize``, times ``scale`` (mpe_select_experts). Current stream."""
-    import torch
     dev = _device(logits)
     types, device, stream, f, _, _ = _ops or _load_ops()
     T, E, ld = _matrix(logits, "logits", dev)
     bptr = 0
     if bias is not None:
-        _vector(bias, E, "bias", dev, (torch.float32,))
+        _vector(bias, E, "bias", dev, (_torch.float32,))
         bptr = bias.data_ptr()
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    elif (ids.dtype != torch.int32 or ids.shape != (T, k) or not ids.is_contiguous()
+        ids = _torch.empty((T, k), dtype=_torch.int32, device=logits.device)
+    elif (ids.dtype != _torch.int32 or ids.shape != (T, k) or not ids.is_contiguous()
           or ids.get_device() != dev):
         raise ValueError(f"ids must be a contiguous int32 [{T}, {k}] on CUDA device {dev}")
     if w is None:
-        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    elif (w.dtype != torch.float32 or w.shape != (T, k) or not w.is_contiguous()
+        w = _torch.empty((T, k), dtype=_torch.float32, device=logits.device)
+    elif (w.dtype != _torch.float32 or w.shape != (T, k) or not w.is_contiguous()
           or w.get_device() != dev):
         raise ValueError(f"w must be a contiguous float32 [{T}, {k}] on CUDA device {dev}")
     args = _SELECT_ARGS.pack(logits.data_ptr(), bptr, ids.data_ptr(), w.data_ptr(), ld, T, E, k,
@@ -337,16 +338,15 @@ def expert_importance(logits, *, score: int = SCORE_SOFTMAX, out=None):
     """float32 [E]: the experts' mean routing scores over a batch of router logits [T, E], the
     importances p that ``allocate_bits`` and ``Context.repage`` take (mpe_expert_importance).
     Current stream."""
-    import torch
     dev = _device(logits)
     types, device, stream, _, f, _ = _ops or _load_ops()
     T, E, ld = _matrix(logits, "logits", dev)
     if out is None:
-        out = torch.empty(E, dtype=torch.float32, device=logits.device)
+        out = _torch.empty(E, dtype=_torch.float32, device=logits.device)
     else:
-        _vector(out, E, "out", dev, (torch.float32,))
+        _vector(out, E, "out", dev, (_torch.float32,))
     need = lib().mpe_expert_importance_workspace(T, E)
-    ws = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
+    ws = _torch.empty(need, dtype=_torch.uint8, device=logits.device) if need else None
     args = _IMPORTANCE_ARGS.pack(logits.data_ptr(), out.data_ptr(), ws.data_ptr() if need else 0, need, ld,
                                  T, E, _type(types, logits, "logits"), score)
     rc = f(args, stream(dev)) if dev == device() else _on(dev, f, args)
@@ -374,12 +374,10 @@ def linear(x, weight, *, bias=None, act: int = ACT_NONE, gated: bool = False, re
     N = R // 2 if gated else R
     bptr = btyp = rptr = ldr = 0
     if bias is not None:
-        import torch
-        _vector(bias, R, "bias", dev, (dtype, torch.float32))
+        _vector(bias, R, "bias", dev, (dtype, _torch.float32))
         bptr, btyp = bias.data_ptr(), types[bias.dtype]
     if out is None:
-        import torch
-        out = torch.empty((M, N), dtype=out_dtype or (dtype if residual is None else residual.dtype),
+        out = _torch.empty((M, N), dtype=out_dtype or (dtype if residual is None else residual.dtype),
                           device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")

@@ -917,18 +917,20 @@ struct Choice {
 };
 
 // The form with the least estimated time, in us, from times measured on B200 over
-// M 1 .. 8192, N 128 .. 14336, K 512 .. 14336:
-//   k_narrow<NT>  starts and ends in 2.4 + 0.047 NT (64 tokens x 128 x 2048, no
-//                 split: 13.4 with NT 32, 14.3 with NT 64); a step takes a CTA
-//                 0.3, or what an SM takes in at 112 GB/s where it has several
-//                 CTAs (128 x 2048 x 2048, NT 64, split 1, 2, 4: 15.4, 10.8, 8.2);
-//                 tiles of tokens that read the same rows of w at once cost 0.06
-//                 each (786 x 48 x 1056: 9.4 with NT 16, 6.9 with 32, 6.3 with 64);
-//                 rows that do not start at 128 bytes cost every step two lines
-//                 instead of one (333 x 4096 x 2048, NT 64: 17; x 2040: 26);
-//                 an SM holds two CTAs (NT 128: one), and a second round starts
-//                 and ends again, mostly hidden (512 x 7168 x 2048: 33 with NT 64
-//                 against 16.9 for k_wide<256>)
+// M 1 .. 8192, N 16 .. 14336, K 64 .. 14336 (of 60 products at random the form taken
+// is within 10% of the best of all forms for 49, at worst 1.27 times it):
+//   k_narrow<NT>  starts and ends in 3.4 + 0.04 NT (one tile, K = 2048, split 8: 3.6
+//                 with NT 16, 4.3, 5.0 and 8.6 with 128); a step takes a CTA 0.24, or
+//                 what an SM takes in at 112 GB/s where it has several CTAs (NT
+//                 tokens x 2048 x 2048, split 1, 2, 4: 11.7, 8.2, 6.2 with NT 16,
+//                 16.2, 13.2, 11.5 with 128); tiles of tokens that read the same rows
+//                 of w at once get in each other's way, 0.003 a tile and step (786 x
+//                 48 x 1056: 9.4 with NT 16, 6.9 with 32, 6.3 with 64); rows that do
+//                 not start at 128 bytes cost every step two lines instead of one
+//                 (333 x 4096 x 2048, NT 64: 17; x 2040: 26); an SM holds three CTAs
+//                 with NT 16, two with 32 and 64, one with 128, and a second round
+//                 starts and ends again, mostly hidden (512 x 7168 x 2048: 33 with NT
+//                 64 against 16.9 for k_wide<256>)
 //   k_wide<BN>    starts and ends in 7 (BN 256: 8), 0.28 a step and round of a
 //                 pair of CTAs (1024 x 2048 x 2048: 15.6 with 256, 16.2 with 128,
 //                 18 for k_narrow<64>; 512 x 2048 x 7168: 38, against 28.5 for
@@ -958,13 +960,13 @@ Choice choose(const mpe_linear_args& p, int sms) {
     for (int nt = 16; nt <= 128 && nt < 2 * p.M + 16; nt *= 2) {
         const int64_t mtiles = (p.M + nt - 1) / nt;
         if (mtiles > 65535) continue;  // the grid's y
-        const double fixed = 2.4 + 0.047 * nt + 0.06 * mtiles, ingest = (kRows + nt) * 128 / 112e3;
+        const double fixed = 3.4 + 0.04 * nt + 0.003 * mtiles * nk, ingest = (kRows + nt) * 128 / 112e3;
         for (int s = 1; s <= 8 && (s == 1 || nk >= 2 * s); s *= 2) {
             const double ctas = (double)ntiles * mtiles * s, slots = nt == 128 ? sms : nt == 16 ? 3 * sms : 2 * sms;
             if (ntiles * s > INT32_MAX) continue;  // the grid's x
             const double rounds = (double)(int64_t)((ctas + slots - 1) / slots);
             const double there = (ctas < slots ? ctas : slots) / sms;  // CTAs an SM
-            const double one = there * ingest > 0.3 ? there * ingest : 0.3, step = lines ? one : 1.7 * one;
+            const double one = there * ingest > 0.24 ? there * ingest : 0.24, step = lines ? one : 1.7 * one;
             offer({false, nt, s}, fixed + 0.7 * fixed * (rounds - 1) + both(rounds * ((nk + s - 1) / s) * step));
         }
     }
