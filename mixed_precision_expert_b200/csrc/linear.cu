@@ -441,7 +441,9 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
 // takes tiles in turn; two accumulators let the MMAs of a tile run while the
 // one before is finished.
 //   warp 0     loads into a ring of K-steps of 64
-//   warp 1     MMAs (rank 0)
+//   warps 1, 2 MMAs (rank 0): with BN 256 one issuing thread, whose MMAs take as
+//              long as issuing them; with BN 128 two, every second step and an
+//              accumulator each, as in k_narrow
 //   warps 4-11 epilogue, 32 tokens and half of the outputs each: a thread has a
 //              token's outputs, which go through 2 KB of shared memory a warp, so
 //              that global memory is read and written in runs of 64 bytes of a row
@@ -453,7 +455,9 @@ struct Wide {
     static constexpr int kStaging = 8 * 2048;
     static constexpr int kSmem = 1024 + kRing + kStaging + 4 * BN * 4 + 256;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-    static constexpr int kCols = 2 * BN;
+    static constexpr int kIssuers = BN == 256 ? 1 : 2;
+    static_assert(kStages % kIssuers == 0, "stages of an issuer");
+    static constexpr int kCols = 2 * kIssuers * BN;
     static_assert(kCols <= 512, "tensor memory");
 };
 constexpr int kWideThreads = 384;
@@ -509,7 +513,7 @@ __device__ __forceinline__ void move_values(uint8_t* stage, void* base, int64_t 
 template <int BN, bool GATED, int SZ>
 __global__ void __launch_bounds__(kWideThreads, 1)
 k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Epilogue e,
-       const Tiles grid, const int nk, const uint32_t idesc) {
+       const Tiles grid, const int nk, const uint32_t idesc) {  // nk: steps, a multiple of kIssuers
     using C = Wide<BN>;
     constexpr int kOut = GATED ? BN / 2 : BN;  // outputs of a tile
     extern __shared__ uint8_t smem_raw[];
@@ -521,8 +525,8 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
     uint64_t* empty = full + C::kStages;                              // each CTA: its stage was multiplied
     uint64_t* acc_full = empty + C::kStages;                          // each CTA: [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by both CTAs' epilogue warps
-    // float32 results: chains of kChain inputs, as in k_narrow; others: all of K
-    const int chain = SZ == 4 ? kChain / kKStep : nk;
+    // float32 results: chains of kChain inputs an accumulator, as in k_narrow; others: all of K
+    const int chain = SZ == 4 ? C::kIssuers * kChain / kKStep : nk;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank();
@@ -537,7 +541,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_full[i], C::kIssuers);
             mbar_init(&acc_empty[i], 16);
         }
         fence_mbar_init();
@@ -586,10 +590,11 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp <= C::kIssuers) {
         if (rank == 0 && lane == 0) {
+            const int x = warp - 1;
             const uint64_t desc = tc::smem_desc(smem_u32(ring));
-            int s = 0, b = 0;
+            int s = x, b = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool again = false;  // both accumulators have been in use
             for (int64_t t = pair; t < tiles && ok; t += pairs) {
@@ -599,9 +604,9 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                         break;
                     }
                     tc::fence_after();
-                    const uint32_t d = tbase + (uint32_t)(b * BN);
+                    const uint32_t d = tbase + (uint32_t)((b * C::kIssuers + x) * BN);
                     const int k1 = min(nk, k0 + chain);
-                    for (int k = k0; k < k1; ++k) {
+                    for (int k = k0 + x; k < k1; k += C::kIssuers) {
                         if (!mbar_wait_spin(&full[s], phase)) {
                             ok = false;
                             break;
@@ -610,9 +615,10 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                         const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (128 * 128 >> 4);
 #pragma unroll
                         for (int i = 0; i < kKStep / 16; ++i)
-                            tc::mma_pair(d, da + 2 * i, db + 2 * i, idesc, k > k0 || i > 0);
+                            tc::mma_pair(d, da + 2 * i, db + 2 * i, idesc, k > k0 + x || i > 0);
                         tc::commit_pair(&empty[s]);
-                        if (++s == C::kStages) s = 0, phase ^= 1u;
+                        s += C::kIssuers;
+                        if (s >= C::kStages) s -= C::kStages, phase ^= 1u;
                     }
                     tc::commit_pair(&acc_full[b]);
                     if (++b == 2) b = 0, acc_phase ^= 1u, again = true;
@@ -666,21 +672,19 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + half * kHalf);
+                    const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::kIssuers * BN + half * kHalf);
 #pragma unroll
-                    for (int g = 0; g < BN / 2; g += 32) {
-                        uint32_t v[2][16];
+                    for (int g = 0; g < BN / 2; g += 16) {
+                        uint32_t v[C::kIssuers][16];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int at = g + 16 * h;
-                            tc::tmem_load16(acc + (uint32_t)(at < kHalf ? at : kOut + at - kHalf), v[h]);
-                        }
+                        for (int x = 0; x < C::kIssuers; ++x)
+                            tc::tmem_load16(acc + (uint32_t)(x * BN + (g < kHalf ? g : kOut + g - kHalf)), v[x]);
                         tc::tmem_wait();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            tc::tmem_ready(v[h]);
+                        for (int x = 0; x < C::kIssuers; ++x) {
+                            tc::tmem_ready(v[x]);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[g + 16 * h + i] += __uint_as_float(v[h][i]);
+                            for (int i = 0; i < 16; ++i) sum[g + i] += __uint_as_float(v[x][i]);
                         }
                     }
                     tc::fence_before();
@@ -692,17 +696,11 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
             if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after();
-            const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + half * kHalf);
+            const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::kIssuers * BN + half * kHalf);
 #pragma unroll(SZ == 4 ? kHalf / kChunk : 1)  // 16-bit: the activations' code once; float32: sum[] is registers
             for (int c = 0; c < kHalf; c += kChunk) {
                 if (!ok) break;
                 if (n0 + c >= e.N || m >= e.M) break;
-                uint32_t v[kChunk / 16][16], u[kChunk / 16][16];
-#pragma unroll
-                for (int h = 0; h < kChunk / 16; ++h) {
-                    tc::tmem_load16(acc + (uint32_t)(c + 16 * h), v[h]);
-                    if (GATED) tc::tmem_load16(acc + (uint32_t)(kOut + c + 16 * h), u[h]);
-                }
                 const bool pieces = whole(c);
                 if (e.residual) {
                     if (pieces) {
@@ -714,17 +712,34 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                     }
                     __syncwarp();
                 }
-                tc::tmem_wait();
+                float f[kChunk], up[kChunk];
 #pragma unroll
-                for (int h = 0; h < kChunk / 16; ++h) {
-                    tc::tmem_ready(v[h]);
-                    if (GATED) tc::tmem_ready(u[h]);
-                }
-                float f[kChunk];
+                for (int h = 0; h < kChunk; h += 16) {
+                    uint32_t v[C::kIssuers][16], u[C::kIssuers][16];
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) {
-                    f[i] = __uint_as_float(v[i / 16][i % 16]);
-                    if constexpr (SZ == 4) f[i] += sum[c + i];
+                    for (int x = 0; x < C::kIssuers; ++x) {
+                        tc::tmem_load16(acc + (uint32_t)(x * BN + c + h), v[x]);
+                        if (GATED) tc::tmem_load16(acc + (uint32_t)(x * BN + kOut + c + h), u[x]);
+                    }
+                    tc::tmem_wait();
+#pragma unroll
+                    for (int x = 0; x < C::kIssuers; ++x) {
+                        tc::tmem_ready(v[x]);
+                        if (GATED) tc::tmem_ready(u[x]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        f[h + i] = __uint_as_float(v[0][i]);
+                        up[h + i] = GATED ? __uint_as_float(u[0][i]) : 0.0f;
+                        if constexpr (C::kIssuers == 2) {
+                            f[h + i] += __uint_as_float(v[1][i]);
+                            if (GATED) up[h + i] += __uint_as_float(u[1][i]);
+                        }
+                        if constexpr (SZ == 4) {
+                            f[h + i] += sum[c + h + i];
+                            if (GATED) up[h + i] += sum[kHalf + c + h + i];
+                        }
+                    }
                 }
                 if (e.bias) {
 #pragma unroll
@@ -733,11 +748,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 activate<kChunk>(f, e.act);
                 if (GATED) {
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) {
-                        float up = __uint_as_float(u[i / 16][i % 16]);
-                        if constexpr (SZ == 4) up += sum[kHalf + c + i];
-                        f[i] *= up + (e.bias ? bias[kHalf + c + i] : 0.0f);
-                    }
+                    for (int i = 0; i < kChunk; ++i) f[i] *= up[i] + (e.bias ? bias[kHalf + c + i] : 0.0f);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -898,7 +909,9 @@ cudaError_t launch_wide(const mpe_linear_args& p, const Epilogue& e, int sms, cu
     attr[1].val.clusterDim = {2, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_wide<BN, GATED, SZ>, mx, mw, e, g, (p.K + kKStep - 1) / kKStep,
+    // steps for every issuer alike: a box past K reads as zeros
+    const int nk = (p.K + kKStep - 1) / kKStep, steps = (nk + C::kIssuers - 1) / C::kIssuers * C::kIssuers;
+    return cudaLaunchKernelEx(&cfg, k_wide<BN, GATED, SZ>, mx, mw, e, g, steps,
                               tc::instr_desc(kTileM, BN, p.type == MPE_TYPE_BF16));
 }
 
@@ -931,10 +944,11 @@ struct Choice {
 //                 with NT 16, two with 32 and 64, one with 128, and a second round
 //                 starts and ends again, mostly hidden (512 x 7168 x 2048: 33 with NT
 //                 64 against 16.9 for k_wide<256>)
-//   k_wide<BN>    starts and ends in 7 (BN 256: 8), 0.28 a step and round of a
-//                 pair of CTAs (1024 x 2048 x 2048: 15.6 with 256, 16.2 with 128,
-//                 18 for k_narrow<64>; 512 x 2048 x 7168: 38, against 28.5 for
-//                 k_narrow<128> with split 2)
+//   k_wide<BN>    starts and ends in 7 (BN 256: 8); a step of a pair of CTAs takes
+//                 0.28 with 256, 0.17 with 128, 0.21 in a second round and later
+//                 (1024 x 2048 x 2048: 12.0 with 128, 16.0 with 256, 18 for
+//                 k_narrow<64>; 512 x 2048 x 7168: 26, 39, and 28.5 for
+//                 k_narrow<128> with split 2; 2048 x 2048 x 768: 11.1, 10.6)
 // and all of them the time of memory at 6 TB/s, which hides most of the steps (or
 // is hidden by them).
 Choice choose(const mpe_linear_args& p, int sms) {
@@ -953,7 +967,7 @@ Choice choose(const mpe_linear_args& p, int sms) {
         const int out = p.gated ? bn / 2 : bn;
         const double tiles = (double)((p.M + kTileM - 1) / kTileM) * ((p.N + out - 1) / out);
         const double rounds = (double)(int64_t)((tiles + sms / 2 - 1) / (sms / 2));
-        offer({true, bn, 1}, (bn == 256 ? 8.0 : 7.0) + both(rounds * nk * 0.28));
+        offer({true, bn, 1}, bn == 256 ? 8.0 + both(rounds * nk * 0.28) : 7.0 + both(rounds * nk * (rounds > 1 ? 0.21 : 0.17)));
     }
     const int64_t ntiles = (p.N + per - 1) / per;
     const bool lines = (p.N == 1 || p.ldw % 64 == 0) && (p.M == 1 || p.ldx % 64 == 0) && aligned(p.w, 128) && aligned(p.x, 128);
