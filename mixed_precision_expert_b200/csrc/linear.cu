@@ -931,7 +931,7 @@ struct Choice {
 
 // The form with the least estimated time, in us, from times measured on B200 over
 // M 1 .. 8192, N 16 .. 14336, K 64 .. 14336 (of 60 products at random the form taken
-// is within 10% of the best of all forms for 49, at worst 1.27 times it):
+// is within 10% of the best of all forms for 51, at worst 1.3 times it):
 //   k_narrow<NT>  starts and ends in 3.4 + 0.04 NT (one tile, K = 2048, split 8: 3.6
 //                 with NT 16, 4.3, 5.0 and 8.6 with 128); a step takes a CTA 0.24, or
 //                 what an SM takes in at 112 GB/s where it has several CTAs (NT
@@ -939,13 +939,14 @@ struct Choice {
 //                 16.2, 13.2, 11.5 with 128); tiles of tokens that read the same rows
 //                 of w at once get in each other's way, 0.003 a tile and step (786 x
 //                 48 x 1056: 9.4 with NT 16, 6.9 with 32, 6.3 with 64); rows that do
-//                 not start at 128 bytes cost every step two lines instead of one
-//                 (333 x 4096 x 2048, NT 64: 17; x 2040: 26); an SM holds three CTAs
+//                 not start at 128 bytes take in two lines instead of one (333 x
+//                 4096 x 2048, NT 64: 17; x 2040: 26); an SM holds three CTAs
 //                 with NT 16, two with 32 and 64, one with 128, and a second round
 //                 starts and ends again, mostly hidden (512 x 7168 x 2048: 33 with NT
 //                 64 against 16.9 for k_wide<256>)
 //   k_wide<BN>    starts and ends in 7 (BN 256: 8); a step of a pair of CTAs takes
-//                 0.28 with 256, 0.17 with 128, 0.21 in a second round and later
+//                 0.28 with 256, 0.17 with 128, 0.21 in a second round and later; a
+//                 round's epilogue hides a short round (4.0, 2.2)
 //                 (1024 x 2048 x 2048: 12.0 with 128, 16.0 with 256, 18 for
 //                 k_narrow<64>; 512 x 2048 x 7168: 26, 39, and 28.5 for
 //                 k_narrow<128> with split 2; 2048 x 2048 x 768: 11.1, 10.6)
@@ -967,7 +968,8 @@ Choice choose(const mpe_linear_args& p, int sms) {
         const int out = p.gated ? bn / 2 : bn;
         const double tiles = (double)((p.M + kTileM - 1) / kTileM) * ((p.N + out - 1) / out);
         const double rounds = (double)(int64_t)((tiles + sms / 2 - 1) / (sms / 2));
-        offer({true, bn, 1}, bn == 256 ? 8.0 + both(rounds * nk * 0.28) : 7.0 + both(rounds * nk * (rounds > 1 ? 0.21 : 0.17)));
+        const double steps = nk * (bn == 256 ? 0.28 : rounds > 1 ? 0.21 : 0.17), epilogue = bn == 256 ? 4.0 : 2.2;
+        offer({true, bn, 1}, (bn == 256 ? 8.0 : 7.0) + both(steps + (rounds - 1) * (steps > epilogue ? steps : epilogue)));
     }
     const int64_t ntiles = (p.N + per - 1) / per;
     const bool lines = (p.N == 1 || p.ldw % 64 == 0) && (p.M == 1 || p.ldx % 64 == 0) && aligned(p.w, 128) && aligned(p.x, 128);
@@ -980,7 +982,7 @@ Choice choose(const mpe_linear_args& p, int sms) {
             if (ntiles * s > INT32_MAX) continue;  // the grid's x
             const double rounds = (double)(int64_t)((ctas + slots - 1) / slots);
             const double there = (ctas < slots ? ctas : slots) / sms;  // CTAs an SM
-            const double one = there * ingest > 0.24 ? there * ingest : 0.24, step = lines ? one : 1.7 * one;
+            const double in = there * ingest * (lines ? 1.0 : 1.9), step = in > 0.24 ? in : 0.24;
             offer({false, nt, s}, fixed + 0.7 * fixed * (rounds - 1) + both(rounds * ((nk + s - 1) / s) * step));
         }
     }
