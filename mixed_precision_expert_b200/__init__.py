@@ -364,26 +364,31 @@ def linear(x, weight, *, bias=None, act: int = ACT_NONE, gated: bool = False, re
     float32 (``out_dtype``, default the residual's or x's) (mpe_linear). Current stream."""
     dev = _device(x)
     types, device, stream, _, _, f = _ops or _load_ops()
-    M, K, ldx = _matrix(x, "x", dev)
-    R, Kw, ldw = _matrix(weight, "weight", dev)
     dtype = x.dtype
+    try:
+        (M, K), (ldx, sx) = x.shape, x.stride()
+        (R, Kw), (ldw, sw) = weight.shape, weight.stride()
+        N = R // 2 if gated else R
+        if out is None:
+            out = _torch.empty((M, N), device=x.device,
+                               dtype=out_dtype or (dtype if residual is None else residual.dtype))
+        (mo, no), (ldo, so) = out.shape, out.stride()
+    except ValueError:
+        raise ValueError("x, weight and out must be matrices") from None
+    if (sx != 1 and K > 1) or (sw != 1 and Kw > 1) or (so != 1 and no > 1):
+        raise ValueError("x, weight and out must have contiguous rows")
+    if weight.get_device() != dev or out.get_device() != dev:
+        raise ValueError(f"weight and out must be on CUDA device {dev}, with x")
     if Kw != K or weight.dtype != dtype:
         raise ValueError(f"weight must be {dtype} [N, {K}]")
     if gated and R % 2:
         raise ValueError("a gated weight has an even number of rows")
-    N = R // 2 if gated else R
+    if mo != M or no != N or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {out_dtype or out.dtype} [{M}, {N}]")
     bptr = btyp = rptr = ldr = 0
     if bias is not None:
         _vector(bias, R, "bias", dev, (dtype, _torch.float32))
         bptr, btyp = bias.data_ptr(), types[bias.dtype]
-    if out is None:
-        out = _torch.empty((M, N), dtype=out_dtype or (dtype if residual is None else residual.dtype),
-                          device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out is {out.dtype}, not {out_dtype}")
-    mo, no, ldo = _matrix(out, "out", dev)
-    if mo != M or no != N:
-        raise ValueError(f"out must be [{M}, {N}]")
     if residual is not None:
         mo, no, ldr = _matrix(residual, "residual", dev)
         if mo != M or no != N or residual.dtype != out.dtype:
