@@ -172,7 +172,7 @@ struct Output {
 //              an accumulator each (a step takes one thread 0.28 us whatever NT and
 //              the number of stages; two overlap: 1 x 128 x 2048 without a split
 //              12.5 -> 7.8 us)
-//   warps 4-7  tensor memory -> shared memory
+//   warps 4-7  tensor memory -> shared memory (all warps, where it is read once)
 //   all        sums over the ranks, epilogue
 // The tensor cores cut what they add to an accumulator instead of rounding it: the
 // error grows by about 10^-9 of the result a value of K, always towards zero
@@ -316,12 +316,34 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
         __syncwarp();
     }
     // the sums of this share of K: lanes 32 (w % 4) .. of tensor memory, a row a thread
-    if (warp >= 4) {
+    const int steps = k_last - k_first, n = ((steps + 1) / 2 + chain - 1) / chain;  // chains of accumulator 0
+    if (n == 1) {
+        // one chain: all warps at its end, w and w + 4 every second 16 tokens
+        ok &= mbar_wait_bounded(&acc_full[0], 0);
+        if (steps > 1) ok &= mbar_wait_bounded(&acc_full[1], 0);
+        ok = __all_sync(0xffffffffu, ok);
+        tc::fence_after();
+        const uint32_t acc = *tmem_slot + ((uint32_t)((warp & 3) * 32) << 16);
+        float* to = part + (warp & 3) * 32 + lane;
+#pragma unroll 1
+        for (int c = (warp >> 2) * 16; c < mt && ok; c += 32) {
+            uint32_t v[2][16];
+            tc::tmem_load16(acc + (uint32_t)c, v[0]);
+            if (steps > 1) tc::tmem_load16(acc + (uint32_t)(NT + c), v[1]);
+            tc::tmem_wait();
+            tc::tmem_ready(v[0]);
+            tc::tmem_ready(v[1]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float s = __uint_as_float(v[0][i]);
+                to[(c + i) * kRows] = steps > 1 ? s + __uint_as_float(v[1][i]) : s;
+            }
+        }
+    } else if (warp >= 4) {
         float sum[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) sum[i] = 0.0f;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int steps = k_last - k_first, n = ((steps + 1) / 2 + chain - 1) / chain;  // chains of accumulator 0
 #pragma unroll 1
         for (int c = 0; c < 2 * n && ok; ++c) {
             const int x = c & 1;
