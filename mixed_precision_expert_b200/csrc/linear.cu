@@ -953,12 +953,12 @@ struct Choice {
 
 // The form with the least estimated time, in us, from times measured on B200 over
 // M 1 .. 8192, N 16 .. 14336, K 64 .. 14336 (of 60 products at random the form taken
-// is within 10% of the best of all forms for 51, at worst 1.3 times it):
-//   k_narrow<NT>  starts and ends in 3.4 + 0.04 NT (one tile, K = 2048, split 8: 3.6
-//                 with NT 16, 4.3, 5.0 and 8.6 with 128); a step takes a CTA 0.24, or
+// is within 10% of the best of all forms for 53, at worst 1.4 times it):
+//   k_narrow<NT>  starts and ends in 3.3 + 0.025 NT (one tile, K = 2048, split 8: 3.8
+//                 with NT 16, 4.1, 4.9 and 6.9 with 128); a step takes a CTA 0.24, or
 //                 what an SM takes in at 112 GB/s where it has several CTAs (NT
-//                 tokens x 2048 x 2048, split 1, 2, 4: 11.7, 8.2, 6.2 with NT 16,
-//                 16.2, 13.2, 11.5 with 128); tiles of tokens that read the same rows
+//                 tokens x 2048 x 2048, split 1, 2, 4: 11.9, 8.3, 6.4 with NT 16,
+//                 14.6, 11.3, 9.6 with 128); tiles of tokens that read the same rows
 //                 of w at once get in each other's way, 0.003 a tile and step (786 x
 //                 48 x 1056: 9.4 with NT 16, 6.9 with 32, 6.3 with 64); rows that do
 //                 not start at 128 bytes take in two lines instead of one (333 x
@@ -968,7 +968,9 @@ struct Choice {
 //                 64 against 16.9 for k_wide<256>)
 //   k_wide<BN>    starts and ends in 7 (BN 256: 8); a step of a pair of CTAs takes
 //                 0.28 with 256, 0.17 with 128, 0.21 in a second round and later; a
-//                 round's epilogue hides a short round (4.0, 2.2)
+//                 round's epilogue hides a short round (4.0, 2.2); rows that do not
+//                 start at 128 bytes cost half as much again (333 x 4096 x 2048 and
+//                 2040 with 128: 13.5, 15.5)
 //                 (1024 x 2048 x 2048: 12.0 with 128, 16.0 with 256, 18 for
 //                 k_narrow<64>; 512 x 2048 x 7168: 26, 39, and 28.5 for
 //                 k_narrow<128> with split 2; 2048 x 2048 x 768: 11.1, 10.6)
@@ -981,6 +983,8 @@ Choice choose(const mpe_linear_args& p, int sms) {
     const double memory =
         (2.0 * p.K * (p.M + wrows) + (p.residual ? 2.0 : 1.0) * type_bytes(p.out_type) * p.M * p.N) / 6e6;
     auto both = [&](double steps) { return (steps > memory ? steps : memory) + 0.25 * (steps > memory ? memory : steps); };
+    // rows that start at 128 bytes
+    const bool lines = (p.N == 1 || p.ldw % 64 == 0) && (p.M == 1 || p.ldx % 64 == 0) && aligned(p.w, 128) && aligned(p.x, 128);
     Choice best{true, 256, 1};
     double least = 1e30;
     auto offer = [&](const Choice& c, double us) {
@@ -990,15 +994,14 @@ Choice choose(const mpe_linear_args& p, int sms) {
         const int out = p.gated ? bn / 2 : bn;
         const double tiles = (double)((p.M + kTileM - 1) / kTileM) * ((p.N + out - 1) / out);
         const double rounds = (double)(int64_t)((tiles + sms / 2 - 1) / (sms / 2));
-        const double steps = nk * (bn == 256 ? 0.28 : rounds > 1 ? 0.21 : 0.17), epilogue = bn == 256 ? 4.0 : 2.2;
+        const double steps = nk * (bn == 256 ? 0.28 : rounds > 1 ? 0.21 : 0.17) * (lines ? 1.0 : 1.5), epilogue = bn == 256 ? 4.0 : 2.2;
         offer({true, bn, 1}, (bn == 256 ? 8.0 : 7.0) + both(steps + (rounds - 1) * (steps > epilogue ? steps : epilogue)));
     }
     const int64_t ntiles = (p.N + per - 1) / per;
-    const bool lines = (p.N == 1 || p.ldw % 64 == 0) && (p.M == 1 || p.ldx % 64 == 0) && aligned(p.w, 128) && aligned(p.x, 128);
     for (int nt = 16; nt <= 128 && nt < 2 * p.M + 16; nt *= 2) {
         const int64_t mtiles = (p.M + nt - 1) / nt;
         if (mtiles > 65535) continue;  // the grid's y
-        const double fixed = 3.4 + 0.04 * nt + 0.003 * mtiles * nk, ingest = (kRows + nt) * 128 / 112e3;
+        const double fixed = 3.3 + 0.025 * nt + 0.003 * mtiles * nk, ingest = (kRows + nt) * 128 / 112e3;
         for (int s = 1; s <= 8 && (s == 1 || nk >= 2 * s); s *= 2) {
             const double ctas = (double)ntiles * mtiles * s, slots = nt == 128 ? sms : nt == 16 ? 3 * sms : 2 * sms;
             if (ntiles * s > INT32_MAX) continue;  // the grid's x
