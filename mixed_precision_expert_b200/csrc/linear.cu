@@ -956,7 +956,7 @@ struct Choice {
 // is within 10% of the best of all forms for 53, at worst 1.4 times it):
 //   k_narrow<NT>  starts and ends in 3.3 + 0.025 NT (one tile, K = 2048, split 8: 3.8
 //                 with NT 16, 4.1, 4.9 and 6.9 with 128); a step takes a CTA 0.24, or
-//                 what an SM takes in at 112 GB/s where it has several CTAs (NT
+//                 what an SM takes in at 105 GB/s where it has several CTAs (NT
 //                 tokens x 2048 x 2048, split 1, 2, 4: 11.9, 8.3, 6.4 with NT 16,
 //                 14.6, 11.3, 9.6 with 128); tiles of tokens that read the same rows
 //                 of w at once get in each other's way, 0.003 a tile and step (786 x
@@ -1001,7 +1001,7 @@ Choice choose(const mpe_linear_args& p, int sms) {
     for (int nt = 16; nt <= 128 && nt < 2 * p.M + 16; nt *= 2) {
         const int64_t mtiles = (p.M + nt - 1) / nt;
         if (mtiles > 65535) continue;  // the grid's y
-        const double fixed = 3.3 + 0.025 * nt + 0.003 * mtiles * nk, ingest = (kRows + nt) * 128 / 112e3;
+        const double fixed = 3.3 + 0.025 * nt + 0.003 * mtiles * nk, ingest = (kRows + nt) * 128 / 105e3;
         for (int s = 1; s <= 8 && (s == 1 || nk >= 2 * s); s *= 2) {
             const double ctas = (double)ntiles * mtiles * s, slots = nt == 128 ? sms : nt == 16 ? 3 * sms : 2 * sms;
             if (ntiles * s > INT32_MAX) continue;  // the grid's x
