@@ -34,6 +34,11 @@ Quantization", llmdb.app summary page):
   Paging": fetch pages, dequantize on the fly; DecDEC summary, 2.2: weight-only
   quantization dequantizes before multiplying with full-precision
   activations), SwiGLU form, top-k weighted combine.
+* ``select``    -- the choice of experts from router logits and the experts'
+  mean routing scores (PagedWeight, "Dynamic Paging": the router decides the
+  experts; "Quality-Aware Quantization": importances p_e).
+* ``linear``    -- a dense product with bias, activation, gate and residual: the
+  router's projection and shared experts.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against closed forms, hand-worked values, exact rational arithmetic or brute
