@@ -359,6 +359,107 @@ __device__ __forceinline__ float nth_top(float v, int n, float& best) {
     return r;
 }
 
+// Token t's ids and weights: a lane with `chosen` has the expert `id` of logit l
+// (-inf in the others) that is number `rank`; lm is the largest chosen logit, m and
+// inv the softmax's maximum and 1 / sum where weights are not divided by their own.
+__device__ __forceinline__ void write_chosen(const SelectArgs& a, int t, bool chosen, int rank, int id, float l, float lm,
+                                             bool broken, bool softmax, float m, float inv) {
+    float s = 0.0f;
+    if (a.renorm) {  // of the chosen logits alone
+        if (chosen && l != -INFINITY) {
+            if (softmax) s = expf(l - lm);
+            // both factors of e^-lm where the scores may be tiny
+            else s = lm < 0.0f ? __fdividef(expf(l - lm), 1.0f + expf(l)) : __fdividef(1.0f, 1.0f + expf(-l));
+        }
+        const float sum = warp_sum(s);
+        s = sum == 0.0f ? 0.0f : a.scale * __fdividef(s, sum);
+    } else if (chosen) {
+        s = a.scale * (softmax ? (l == -INFINITY ? 0.0f : expf(l - m) * inv) : 1.0f / (1.0f + expf(-l)));
+    }
+    if (chosen) {
+        a.ids[(size_t)t * a.k + rank] = id;
+        a.w[(size_t)t * a.k + rank] = broken ? NAN : s;
+    }
+}
+
+// ---- 16-bit logits, at most 128 experts, no bias, no groups ------------------------------------
+// The logit's 19 bits (sign, exponent and 10 bits of bf16 or f16 as a float, in an
+// order-preserving form) and the expert's index below them are one integer that no
+// other expert has: a lane sorts its own, and the warp's largest is taken k times,
+// which settles ties, infinities and NaN on the way. Up to 128 experts: 8192 x 128
+// bf16 5.4 us, and 8.6 with k_select, whose threshold takes any key; 32768 x 128
+// 16.8 and 24.5; but 32768 x 256 31.3 and 26.4, since a lane moves its keys up k times.
+constexpr uint32_t kIndexBits = 0x1FFFu;  // above MPE_MAX_EXPERTS
+
+// In 1 comparison for 2 keys, 5 for 4.
+template <int EPL>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[EPL]) {
+    auto order = [&](int i, int j) {
+        const uint32_t hi = max(v[i], v[j]), lo = min(v[i], v[j]);
+        v[i] = hi;
+        v[j] = lo;
+    };
+    if constexpr (EPL == 2) order(0, 1);
+    if constexpr (EPL == 4) order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+}
+
+template <typename T, int EPL>
+__global__ void __launch_bounds__(32 * kSelWarps) k_select16(const SelectArgs a) {
+    static_assert(sizeof(T) == 2 && EPL <= 4 && MPE_MAX_EXPERTS <= kIndexBits, "the keys' parts");
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = (gridDim.x * blockDim.x) >> 5;
+    const bool softmax = a.score == MPE_SCORE_SOFTMAX;
+    const int e0 = lane * EPL, n = max(0, min(EPL, a.E - e0));
+    for (int t = blockIdx.x * kSelWarps + warp; t < a.T; t += warps) {
+        const T* row = static_cast<const T*>(a.logits) + (size_t)t * a.ld;
+        float x[EPL];
+        load_row<T, EPL>(row + e0, n, a.wide, x);
+        // NaN, and +inf under the softmax, make the row's weights NaN
+        const float most = softmax ? FLT_MAX : INFINITY;
+        bool broken = false;
+        uint32_t v[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            broken |= !(x[i] <= most);
+            const uint32_t b = __float_as_uint(x[i] + 0.0f);  // -0 as +0
+            const uint32_t up = b ^ (uint32_t)(((int32_t)b >> 31) | (int32_t)0x80000000);
+            v[i] = (x[i] == x[i] ? up & ~kIndexBits : 0u) | (kIndexBits - (uint32_t)(e0 + i));
+            if (i >= n) v[i] = 0u;
+        }
+        broken = __any_sync(kFull, broken);
+        sort_descending<EPL>(v);
+        uint32_t mine = 0u, first = 0u;
+#pragma unroll 4
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t best = __reduce_max_sync(kFull, v[0]);
+            if (v[0] == best) {
+#pragma unroll
+                for (int i = 0; i + 1 < EPL; ++i) v[i] = v[i + 1];
+                v[EPL - 1] = 0u;
+            }
+            if (lane == j) mine = best;
+            if (j == 0) first = best;
+        }
+        auto logit = [](uint32_t u) {
+            return __uint_as_float(u & 0x80000000u ? (u ^ 0x80000000u) & ~kIndexBits : ~u & ~kIndexBits);
+        };
+        const float lm = logit(first);
+        float inv = 0.0f;
+        if (softmax && !a.renorm) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) sum += x[i] == -INFINITY ? 0.0f : expf(x[i] - lm);
+            sum = warp_sum(sum);
+            inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+        }
+        const bool chosen = lane < a.k;
+        write_chosen(a, t, chosen, lane, (int)(kIndexBits - (mine & kIndexBits)), chosen ? logit(mine) : -INFINITY, lm, broken,
+                     softmax, lm, inv);
+    }
+}
+
 template <typename T, int EPL>
 __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 : 3) k_select(const SelectArgs a) {
     __shared__ __align__(16) float s_key[kSelWarps][32];
@@ -587,31 +688,17 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
         }
         const bool chosen = rank < a.k;
         if (!chosen) l = -INFINITY;
-        // weights: of the chosen logits alone where their sum divides them
-        float s = 0.0f;
-        if (a.renorm) {
-            const float lm = warp_top(l);
-            if (chosen && l != -INFINITY) {
-                if (softmax) s = expf(l - lm);
-                // both factors of e^-lm where the scores may be tiny
-                else s = lm < 0.0f ? __fdividef(expf(l - lm), 1.0f + expf(l)) : __fdividef(1.0f, 1.0f + expf(-l));
-            }
-            const float sum = warp_sum(s);
-            s = sum == 0.0f ? 0.0f : a.scale * __fdividef(s, sum);
-        } else if (chosen) {
-            s = a.scale * (softmax ? (l == -INFINITY ? 0.0f : expf(l - m) * inv) : 1.0f / (1.0f + expf(-l)));
-        }
-        if (chosen) {
-            a.ids[(size_t)t * a.k + rank] = id;
-            a.w[(size_t)t * a.k + rank] = broken ? NAN : s;
-        }
+        write_chosen(a, t, chosen, rank, id, l, warp_top(l), broken, softmax, m, inv);
     }
 }
 
 template <typename T, int EPL>
 cudaError_t launch_select(const SelectArgs& a, int sms, cudaStream_t st) {
-    const int64_t want = ((int64_t)a.T + kSelWarps - 1) / kSelWarps, most = (int64_t)sms * 8;
-    return launch_pdl(k_select<T, EPL>, dim3((unsigned)(want < most ? want : most)), dim3(32 * kSelWarps), 0, st, a);
+    const int64_t want = ((int64_t)a.T + kSelWarps - 1) / kSelWarps;
+    const dim3 grid((unsigned)(want < (int64_t)sms * 8 ? want : (int64_t)sms * 8)), block(32 * kSelWarps);
+    if constexpr (sizeof(T) == 2 && EPL <= 4)
+        if (!a.bias && a.keep == a.n_groups) return launch_pdl(k_select16<T, EPL>, grid, block, 0, st, a);
+    return launch_pdl(k_select<T, EPL>, grid, block, 0, st, a);
 }
 
 template <typename T>

@@ -151,6 +151,37 @@ def test_infinities_and_nan_stay_in_their_rows(mpe):
         assert torch.isnan(mpe.linear(x, w, act=mpe.ACT_RELU)[2]).all()
 
 
+def test_offsets_past_32_bits(mpe):
+    """2.3e9 outputs of one product, and rows of x, w, residual and out 2^28 values apart."""
+    M, N, K = 140_000, 16_384, 16
+    x, w = grid(M, K, 0.125, "bf16", 61, 0), grid(N, K, 0.125, "bf16", 62, 0)
+    out = mpe.linear(x, w)
+    rows = torch.tensor([0, 1, 131_071, 131_072, M - 1]).cuda()
+    want = rounded(oln.linear(f64(x[rows]), f64(w)), "bf16")
+    assert torch.equal(out[rows].cpu(), want)
+    for first in range(0, M, 20_000):  # all of it, on the device: exact products, rounded once
+        part = x[first:first + 20_000].double() @ w.double().t()
+        assert torch.equal(out[first:first + 20_000], part.to(torch.bfloat16))
+    del part
+    flat = out.view(-1)[:8 * 2 ** 28].view(8, 2 ** 28)
+    for m, n, k in ((8, 8, 256), (5, 8, 100)):
+        xs, ws = flat[:m, 0:k], flat[:n, 4096:4096 + k]
+        xs.copy_(grid(m, k, 0.125, "bf16", 63, 0))
+        ws.copy_(grid(n, k, 0.125, "bf16", 64, 0))
+        o, r = flat[:m, 1 << 20:(1 << 20) + n], flat[:m, 1 << 21:(1 << 21) + n]
+        r.copy_(grid(m, n, 0.5, "bf16", 65, 0))
+        mpe.linear(xs, ws, residual=r, out=o)
+        assert torch.equal(o.cpu(), rounded(oln.linear(f64(xs), f64(ws), residual=f64(r)), "bf16"))
+
+
+def test_many_tokens_few_outputs(mpe):
+    """More token tiles than a grid's y has."""
+    for M, N, K in ((1_200_000, 8, 16), (1_100_000, 3, 8)):
+        x, w = grid(M, K, 0.125, "bf16", 66, 0), grid(N, K, 0.125, "bf16", 67, 0)
+        want = (x.double() @ w.double().t()).to(torch.bfloat16)
+        assert torch.equal(mpe.linear(x, w), want)
+
+
 def test_overflow_of_a_16_bit_result(mpe):
     x, w = torch.full((3, 64), 200.0).half().cuda(), torch.full((64, 64), 200.0).half().cuda()
     assert torch.isposinf(mpe.linear(x, w)).all()              # 2.56e6

@@ -212,6 +212,43 @@ def test_on_another_stream_and_in_a_graph(mpe):
     assert torch.equal(ids, want[0]) and torch.equal(w, want[1]) and torch.equal(p, p_want)
 
 
+def test_every_16_bit_logit_in_order(mpe):
+    """All bf16 and f16 values, signed zeros, infinities, subnormals and NaNs among them."""
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16)
+    order = torch.randperm(1 << 16, generator=torch.Generator().manual_seed(12))
+    for dtype in (torch.bfloat16, torch.float16):
+        l = bits[order].view(dtype).reshape(-1, 256).cuda()
+        for score in ("softmax", "sigmoid"):
+            l64 = l.double().cpu().numpy()
+            for k, renorm in ((8, True), (32, False)):
+                ids, w = mpe.select_experts(l, k, score=getattr(mpe, "SCORE_" + score.upper()), renormalize=renorm)
+                assert np.array_equal(ids.cpu().numpy(), osel.select_experts(l64, k, score=score, renormalize=renorm)[0])
+                broken = np.isnan(l64).any(axis=1) | (np.isposinf(l64).any(axis=1) if score == "softmax" else False)
+                assert np.array_equal(torch.isnan(w).all(dim=1).cpu().numpy(), broken)
+                assert np.array_equal(torch.isnan(w).any(dim=1).cpu().numpy(), broken)
+
+
+def test_offsets_past_32_bits(mpe):
+    """2.3e9 logits in one matrix, and rows 2^28 values apart."""
+    T, E = 9_000_000, 256
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(13)
+    rows = torch.tensor([0, 1, 8_388_607, 8_388_608, 8_388_609, T - 2, T - 1])
+    l[rows.cuda()] = torch.randn(len(rows), E, generator=g).bfloat16().cuda()
+    ids, w = mpe.select_experts(l, 1)
+    rid, _ = osel.select_experts(l[rows.cuda()].double().cpu().numpy(), 1)
+    assert np.array_equal(ids[rows.cuda()].cpu().numpy(), rid)
+    assert int(ids.count_nonzero()) == int((rid != 0).sum())          # the rows of zeros choose expert 0
+    # nearly every score is 1/256, summed over 9e6 tokens: the order of the sums decides nothing
+    p = mpe.expert_importance(l).double().cpu().numpy()
+    assert np.abs(p * E - 1).max() <= (256 + 17 + 80) * U + len(rows) * E / T
+    flat = l.view(-1)[:8 * 2 ** 28]
+    view = flat.view(8, 2 ** 28)[:, :E]
+    view.copy_(torch.randn(8, E, generator=g).bfloat16())
+    check(mpe, view, 8)
+    check(mpe, view, 8, bias=torch.zeros(E).cuda())
+
+
 @pytest.mark.parametrize("E", [1, 8, 33, 128, 200, 256, 500, 1024])
 @pytest.mark.parametrize("T", [1, 15, 16, 17, 100, 5000])
 def test_importance(mpe, T, E):
