@@ -108,27 +108,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same in two halves.
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address of shared address `a` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-// `bytes` (a multiple of 16) of this CTA's shared memory to a peer's, counted on
-// the peer's barrier (both addresses from peer_addr).
-__device__ __forceinline__ void copy_to_peer(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "r"(smem_u32(src)), "r"(bytes), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void add4(float (&a)[4], const float4& b) {
-    a[0] += b.x, a[1] += b.y, a[2] += b.z, a[3] += b.w;
+// V (4 or 1) floats at a peer's shared address (from peer_addr).
+template <int V>
+__device__ __forceinline__ void peer_load(uint32_t a, float (&v)[V]) {
+    if constexpr (V == 4)
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "r"(a));
+    else
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[0]) : "r"(a));
 }
 
 // ---- pairs of CTAs (cta_group::2): ranks 0 and 1 of a cluster of 2 ----
