@@ -4,8 +4,9 @@ Inputs are small multiples of powers of two, so that every product and every
 partial sum is a multiple of 2^-6 below 2^18 and exact in float32 in any order:
 without an activation the result is the exact value rounded once, and a product
 that is missing, doubled or misplaced shows. An activation of the exact v is off by
-at most |v| 2^-19 (exponential 2 ulp, error function 4 ulp on an argument that is
-off by 2 ulp, a division); its result is rounded once more."""
+at most |v| 2^-19: a sigmoid by 2^-22 and the rounding of its argument, the normal
+distribution function by 7.5e-8, both with a reciprocal and a product of 1 ulp, times
+v. Its result is rounded once more."""
 import numpy as np
 import pytest
 import torch
