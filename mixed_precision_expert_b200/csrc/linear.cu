@@ -998,7 +998,7 @@ Choice choose(const mpe_linear_args& p, int sms) {
         offer({true, bn, 1}, (bn == 256 ? 8.0 : 7.0) + both(steps + (rounds - 1) * (steps > epilogue ? steps : epilogue)));
     }
     const int64_t ntiles = (p.N + per - 1) / per;
-    for (int nt = 16; nt <= 128 && nt < 2 * p.M + 16; nt *= 2) {
+    for (int nt = 16; nt <= 128 && nt / 2 < p.M + 8; nt *= 2) {  // the next above M, too
         const int64_t mtiles = (p.M + nt - 1) / nt;
         if (mtiles > 65535) continue;  // the grid's y
         const double fixed = 3.3 + 0.025 * nt + 0.003 * mtiles * nk, ingest = (kRows + nt) * 128 / 105e3;
