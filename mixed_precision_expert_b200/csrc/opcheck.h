@@ -32,15 +32,19 @@ struct Block {
     int64_t pitch, width, rows;
     Block(const void* p, int64_t r, int64_t cols, int64_t ld, int sz)
         : base(reinterpret_cast<uintptr_t>(p)), pitch(r > 1 ? ld * sz : cols * sz), width(cols * sz), rows(r) {}
-    uintptr_t end() const { return base + (uintptr_t)((rows - 1) * pitch + width); }
+    uintptr_t end() const {
+        if (rows > 1 && pitch > (INT64_MAX / 4) / rows) return UINTPTR_MAX;  // more than any memory
+        return base + (uintptr_t)((rows - 1) * pitch + width);
+    }
 };
 
-// Whether two blocks share a byte. Blocks of one pitch whose spans interleave
-// (columns of one buffer) share none when their columns do not meet; blocks of
-// different pitches count as overlapping when their spans do.
+// Whether two blocks share a byte. Blocks of one pitch (or one row and any block)
+// whose spans interleave, columns of one buffer, share none when their columns do
+// not meet; blocks of different pitches count as overlapping when their spans do.
 inline bool overlap(const Block& p, const Block& q) {
     if (p.end() <= q.base || q.end() <= p.base) return false;
-    if (p.rows > 1 && q.rows > 1 && p.pitch == q.pitch) {
+    if (p.rows == 1 && q.rows > 1) return overlap(q, p);
+    if (p.rows > 1 && (q.rows == 1 || p.pitch == q.pitch)) {
         // where q's rows start in p's
         const int64_t at = q.base >= p.base ? (int64_t)(q.base - p.base) % p.pitch
                                             : (p.pitch - (int64_t)(p.base - q.base) % p.pitch) % p.pitch;

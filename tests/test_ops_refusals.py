@@ -77,6 +77,8 @@ def linear(mpe, x=P, w=2 * P, bias=0, residual=0, out=1 << 40, ldx=64, ldw=64, l
     # out over an input
     dict(out=P), dict(out=2 * P), dict(out=P + 16), dict(out=2 * P + 128 * 128 - 16), dict(bias=(1 << 40) + 128),
     dict(out=2 * P + 128 * 128 - 16, gated=1, N=64, ldo=64),
+    dict(M=1, out=2 * P + 112, ldw=192), dict(M=1, out=2 * P + 256, ldw=192), dict(M=1, out=2 * P - 128),
+    dict(M=1 << 30, ldo=1 << 37, out=1 << 30, x=1 << 40, w=1 << 45),
     # a residual over out that is not out
     dict(residual=(1 << 40) + 256), dict(residual=(1 << 40), ldr=136), dict(residual=(1 << 40) + 16)])
 def test_linear_refuses(mpe, bad):
@@ -89,6 +91,7 @@ def test_linear_refuses(mpe, bad):
     dict(out=P + 128, ldx=128, ldo=128, N=64, w=1 << 30),                      # columns of one buffer: x | out
     dict(x=P + 128, out=P, ldx=128, ldo=128, N=64, w=1 << 30),                 # out | x
     dict(residual=(1 << 40) + 256, ldo=256, ldr=256),                          # out | residual
+    dict(M=1, out=2 * P + 128, ldw=192),                                       # a row beside w's columns
     dict(M=1, out=P + 128, w=1 << 30), dict(bias=P * 9), dict(bias=P * 9, btyp=0, otyp=0)])
 def test_linear_takes(mpe, good):
     """Arguments that pass every check fail later, for want of a device."""
