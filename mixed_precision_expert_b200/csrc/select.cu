@@ -6,6 +6,7 @@
 
 #include "internal.h"
 #include "opcheck.h"
+#include "tc.cuh"
 
 namespace mpe {
 
@@ -738,21 +739,21 @@ bool wide_rows(const void* logits, int32_t type, int64_t ld, int T, int groups, 
 struct ImportanceArgs {
     const void* logits;
     int64_t ld;
-    float* out;   // [E], or null: this CTA's sums go to part
+    float* out;   // [E] (the CTAs are a cluster), or null: this CTA's sums go to part
     float* part;  // [CTAs][E]
     int T, E, score, wide;  // wide: rows are whole, aligned pieces of 16 bytes
 };
 
-constexpr int kImpWarps = 16;
+constexpr int kImpWarps = 16, kImpCluster = 8;
 
 // One warp a token, its columns added up in registers over the tokens; then over
-// the CTA's warps, and over the CTAs in k_importance_join, always in the same
-// order. Which columns a lane has does not matter: pieces of 16 bytes, the warp's
-// next to each other (single values where rows are not aligned to that). A lane
-// copies its pieces of the rows to come asynchronously into its own part of shared
-// memory, so that enough rows are on their way to keep memory busy while a row's
-// maximum and sum go round the warp. The fast exponential: 2 + 1.2 d ulp for a
-// score of e^-d.
+// the CTA's warps, and over the CTAs (in shared memory where they are a cluster,
+// else in k_importance_join), always in the same order. Which columns a lane has
+// does not matter: pieces of 16 bytes, the warp's next to each other (single values
+// where rows are not aligned to that). A lane copies its pieces of the rows to come
+// asynchronously into its own part of shared memory, so that enough rows are on
+// their way to keep memory busy while a row's maximum and sum go round the warp.
+// The fast exponential: 2 + 1.2 d ulp for a score of e^-d.
 template <typename T, int EPL>
 struct ImpRing {
     static constexpr int kRowBytes = 32 * EPL * (int)sizeof(T);
@@ -856,9 +857,23 @@ __global__ void __launch_bounds__(32 * kImpWarps) k_importance(const ImportanceA
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kImpWarps; ++w) s += s_sum[w * 32 * EPL + e];
-        if (a.out) a.out[e] = (float)((double)s / a.T);
-        else a.part[(size_t)blockIdx.x * a.E + e] = s;
+        if (!a.out) a.part[(size_t)blockIdx.x * a.E + e] = s;
+        else if (gridDim.x == 1) a.out[e] = (float)((double)s / a.T);
+        else s_sum[e] = s;  // of column e only this thread reads here
     }
+    if (!a.out || gridDim.x == 1) return;
+    tc::cluster_sync();
+    for (int e = (int)(blockIdx.x * blockDim.x + threadIdx.x); e < a.E; e += (int)(gridDim.x * blockDim.x)) {
+        const uint32_t at = smem_u32(&s_sum[e]);
+        float s[kImpCluster][1];
+#pragma unroll
+        for (int r = 0; r < kImpCluster; ++r) tc::peer_load<1>(tc::peer_addr(at, r), s[r]);
+        double sum = 0.0;
+#pragma unroll
+        for (int r = 0; r < kImpCluster; ++r) sum += (double)s[r][0];
+        a.out[e] = (float)(sum / a.T);
+    }
+    tc::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 // out[e] = 1/T sum over the parts: 32 experts a CTA, every 32nd part a warp.
@@ -878,15 +893,26 @@ __global__ void __launch_bounds__(1024) k_importance_join(const float* part, int
     if (lane == 0 && blockIdx.x * 32 + warp < E) out[blockIdx.x * 32 + warp] = (float)(s / T);
 }
 
-// CTAs, each with sums of its own: one for a few tokens (a second launch costs
-// more than 16 tokens a warp do), else two to an SM, and more where a warp would
+// CTAs, each with sums of its own, and whether they join them in the same launch: one
+// for a few tokens; a cluster, whose CTAs read each other's sums, while its four rows
+// a warp take no longer than two launches do (device / call back to back, cluster and
+// one CTA: 256 x 128 2.9 / 5.2 and 5.4 / 5.5 us, 64 x 256 3.1 / 5.1 and 3.2 / 5.2, 32 x
+// 128 2.6 / 5.3 and 1.9 / 5.2; cluster and two launches, with the workspace's
+// allocation: 512 x 128 3.3 / 5.2 and 3.3 / 9.6, 512 x 256 bf16 4.2 / 5.2 and 3.9 / 9.6,
+// 2048 x 256 7.8 / 8.3 and 4.6 / 9.6); else two to an SM, and more where a warp would
 // add up over 256 rows in float32.
-int importance_parts(int T) {
+struct ImportancePlan {
+    int parts;
+    bool join;  // in the same launch
+};
+ImportancePlan importance_plan(int T, int E) {
+    const int64_t size = (int64_t)T * E;
+    if (T <= 64 && size <= 1 << 14) return {1, true};
+    if (T <= 512 && size <= 1 << 18) return {kImpCluster, true};
     const int most = 296, rows = 256 * kImpWarps;
-    if (T <= 16 * kImpWarps) return 1;
     const int n = (int)(((int64_t)T + kImpWarps - 1) / kImpWarps);
     const int long_run = (int)(((int64_t)T + rows - 1) / rows);
-    return n < most ? n : (long_run > most ? long_run : most);
+    return {n < most ? n : (long_run > most ? long_run : most), false};
 }
 
 template <typename T, int EPL>
@@ -895,7 +921,19 @@ cudaError_t launch_importance(const ImportanceArgs& a, int parts, cudaStream_t s
     cudaError_t e = cudaFuncSetAttribute(k_importance<T, EPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_importance<T, EPL>, dim3(parts), dim3(32 * kImpWarps), smem, st, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(parts);
+    cfg.blockDim = dim3(32 * kImpWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)kImpCluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = a.out && parts > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_importance<T, EPL>, a);
 }
 
 template <typename T>
@@ -985,8 +1023,8 @@ extern "C" int mpe_select_experts(const mpe_select_args* p, void* stream) {
 
 extern "C" size_t mpe_expert_importance_workspace(int32_t T, int32_t E) {
     if (T < 1 || E < 1 || E > MPE_MAX_EXPERTS) return 0;
-    const int parts = importance_parts(T);
-    return parts > 1 ? (size_t)parts * E * sizeof(float) : 0;
+    const ImportancePlan how = importance_plan(T, E);
+    return how.join ? 0 : (size_t)how.parts * E * sizeof(float);
 }
 
 extern "C" int mpe_expert_importance(const mpe_importance_args* p, void* stream) {
@@ -1004,18 +1042,18 @@ extern "C" int mpe_expert_importance(const mpe_importance_args* p, void* stream)
     const Block ws(p->workspace, 1, (int64_t)need, 0, 1);
     if (overlap(out, logits) || (need && (overlap(ws, logits) || overlap(ws, out))))
         return report_global_errorf(MPE_ERR_INVALID, "%s: p_out or the workspace overlaps another argument", who);
-    const int parts = importance_parts(p->T);
+    const ImportancePlan how = importance_plan(p->T, p->E);
     int lanes = 1;
     const int epl = experts_per_lane(1, p->E, &lanes), sz = type_bytes(p->type);
     const bool pieces = aligned(p->logits, 16) && (p->T == 1 || p->ld * sz % 16 == 0) && p->E * sz % 16 == 0;
-    const ImportanceArgs a{p->logits, p->ld, parts > 1 ? nullptr : p->p_out, static_cast<float*>(p->workspace), p->T,
+    const ImportanceArgs a{p->logits, p->ld, how.join ? p->p_out : nullptr, static_cast<float*>(p->workspace), p->T,
                            p->E, p->score, pieces};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = p->type == MPE_TYPE_F32    ? launch_importance_t<float>(a, epl, parts, st)
-                    : p->type == MPE_TYPE_BF16 ? launch_importance_t<__nv_bfloat16>(a, epl, parts, st)
-                                               : launch_importance_t<__half>(a, epl, parts, st);
-    if (e == cudaSuccess && parts > 1)
-        e = launch_pdl(k_importance_join, dim3((p->E + 31) / 32), dim3(1024), 0, st, (const float*)a.part, parts,
+    cudaError_t e = p->type == MPE_TYPE_F32    ? launch_importance_t<float>(a, epl, how.parts, st)
+                    : p->type == MPE_TYPE_BF16 ? launch_importance_t<__nv_bfloat16>(a, epl, how.parts, st)
+                                               : launch_importance_t<__half>(a, epl, how.parts, st);
+    if (e == cudaSuccess && !how.join)
+        e = launch_pdl(k_importance_join, dim3((p->E + 31) / 32), dim3(1024), 0, st, (const float*)a.part, how.parts,
                        p->E, p->T, p->p_out);
     return launched(who, e);
 }

@@ -261,6 +261,26 @@ def test_importance(mpe, T, E):
             assert (np.abs(p - ref) <= importance_tol(l64, ref)).all()
 
 
+@pytest.mark.parametrize("T,E", [(16, 1024), (17, 1024), (64, 256), (64, 257), (65, 8), (129, 1000), (256, 1024),
+                                 (257, 1024), (512, 512), (512, 513), (513, 64)])
+def test_importance_around_the_cluster(mpe, T, E):
+    """Sizes on both sides of one CTA, a cluster of them and two launches; rows whole and not; two calls at once."""
+    for dtype in ("f32", "f16"):
+        for pad in (0, 3):
+            l = torch.nn.functional.pad(logits(T, E, dtype, seed=14), (0, pad))[:, :E]
+            l64 = l.double().cpu().numpy()
+            ref = osel.expert_importance(l64, "softmax")
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            out = []
+            for i in range(8):
+                with torch.cuda.stream(side if i % 2 else torch.cuda.current_stream()):
+                    out.append(mpe.expert_importance(l))
+            torch.cuda.synchronize()
+            assert all(torch.equal(out[0], p) for p in out)
+            assert (np.abs(out[0].double().cpu().numpy() - ref) <= importance_tol(l64, ref)).all()
+
+
 def test_importance_of_masked_and_broken_rows(mpe):
     l = logits(40, 64, seed=10)
     l[0] = -INF
