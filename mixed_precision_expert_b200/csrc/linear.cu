@@ -199,12 +199,15 @@ struct Output {
 //   all        sums over the ranks, epilogue
 // The tensor cores cut what they add to an accumulator instead of rounding it: the
 // error grows by about 10^-9 of the result a value of K, always towards zero
-// (measured: 1.6e-5 at K = 14336). That is nothing beside the rounding of a 16-bit
-// result; for a float32 result an accumulator starts again every kChain inputs,
-// and warps 4-7 add the chains up in registers, rounding to nearest.
+// (measured: 1.6e-5 at K = 14336). So an accumulator starts again every chain_of()
+// inputs, and warps 4-7 add the chains up in registers, rounding to nearest.
 constexpr int kKStep = 64;
 constexpr int kRows = 128;
-constexpr int kChain = 512;
+
+// Inputs that an accumulator takes: 512 for a float32 result (error 4.8e-7 at K =
+// 14336); 1024 for a 16-bit one, whose half step is 250 times what they lose, so that
+// the share of K that a CTA of k_narrow has is most often one chain.
+__host__ __device__ constexpr int chain_of(int out_bytes) { return out_bytes == 4 ? 512 : 1024; }
 
 template <int NT>
 struct Narrow {
@@ -463,13 +466,22 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
 // takes tiles in turn; two accumulators let the MMAs of a tile run while the
 // one before is finished.
 //   warp 0     loads into a ring of K-steps of 64
-//   warps 1, 2 MMAs (rank 0): with BN 256 one issuing thread, whose MMAs take as
-//              long as issuing them; with BN 128 two, every second step and an
-//              accumulator each, as in k_narrow
+//   warps 1, 2 MMAs (rank 0): with BN 256 an issuing thread's MMAs take as long as
+//              issuing them, so two take the chains in turn, and what one does
+//              between two chains passes while the other's run; with BN 128 two
+//              share every chain, every second step and an accumulator each, as in
+//              k_narrow
 //   warps 4-11 epilogue, 32 tokens and half of the outputs each: a thread has a
 //              token's outputs, which go through 2 KB of shared memory a warp, so
 //              that global memory is read and written in runs of 64 bytes of a row
-template <int BN>
+// CHAINED (K beyond one chain of chain_of() inputs an accumulator): the epilogue warps
+// add every chain to sums in registers, 128 a thread with BN 256: warps 0-3 leave
+// theirs to warps 4-11 (setmaxnreg). The accumulator is free again before the
+// epilogue begins. Against one chain that costs 3% of the time (8192 x 2 x 2048 x
+// 7168 gated: 322 -> 332 us, 4096 x 4096 x 4096: 99 -> 103), 5% where one round of
+// tiles leaves the epilogue uncovered (2048 x 2048 x 7168: 46.5 -> 48.8); chains of
+// 2048 inputs would cost 0.7% less.
+template <int BN, bool CHAINED>
 struct Wide {
     static constexpr int kStageBytes = 128 * 128 + BN / 2 * 128;
     static constexpr int kStages = BN == 256 ? 6 : 8;
@@ -481,6 +493,9 @@ struct Wide {
     static_assert(kStages % kIssuers == 0, "stages of an issuer");
     static constexpr int kCols = 2 * kIssuers * BN;
     static_assert(kCols <= 512, "tensor memory");
+    // registers a thread: at the launch, then of warps 0-3 and of warps 4-11
+    static constexpr int kRegs = 168, kFewRegs = BN == 256 ? 40 : 72, kManyRegs = BN == 256 ? 232 : 216;
+    static_assert(kFewRegs + 2 * kManyRegs <= 3 * kRegs, "a split of what the block has");
 };
 constexpr int kWideThreads = 384;
 constexpr int kTileM = 256;
@@ -532,11 +547,11 @@ __device__ __forceinline__ void move_values(uint8_t* stage, void* base, int64_t 
     }
 }
 
-template <int BN, bool GATED, int SZ>
+template <int BN, bool GATED, int SZ, bool CHAINED>
 __global__ void __launch_bounds__(kWideThreads, 1)
 k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Epilogue e,
        const Tiles grid, const int nk, const uint32_t idesc) {  // nk: steps, a multiple of kIssuers
-    using C = Wide<BN>;
+    using C = Wide<BN, CHAINED>;
     constexpr int kOut = GATED ? BN / 2 : BN;  // outputs of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -547,9 +562,9 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
     uint64_t* empty = full + C::kStages;                              // each CTA: its stage was multiplied
     uint64_t* acc_full = empty + C::kStages;                          // each CTA: [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by both CTAs' epilogue warps
-    // float32 results: chains of kChain inputs an accumulator, as in k_narrow; others: all of K
-    const int chain = SZ == 4 ? C::kIssuers * kChain / kKStep : nk;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    const int chain = CHAINED ? C::kIssuers * chain_of(SZ) / kKStep : nk;  // steps of all issuers
+    uint64_t* turn = acc_empty + 2;                                   // rank 0: [2] an issuer's chain is next
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank();
     const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
@@ -565,6 +580,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], C::kIssuers);
             mbar_init(&acc_empty[i], 16);
+            mbar_init(&turn[i], 1);
         }
         fence_mbar_init();
     }
@@ -577,6 +593,10 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
     if (threadIdx.x == 0) griddep_launch_dependents();
     const uint32_t tbase = *tmem_slot;
     bool ok = true;
+    if constexpr (CHAINED) {
+        if (warp < 4) tc::fewer_registers<C::kFewRegs>();
+        else tc::more_registers<C::kManyRegs>();
+    }
 
     if (warp == 0) {
         if (lane == 0) {
@@ -612,38 +632,57 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 }
         }
         __syncwarp();
-    } else if (warp <= C::kIssuers) {
+    } else if (warp <= 2) {
         if (rank == 0 && lane == 0) {
             const int x = warp - 1;
             const uint64_t desc = tc::smem_desc(smem_u32(ring));
-            int s = x, b = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            bool again = false;  // both accumulators have been in use
+            int s = C::kIssuers == 2 ? x : 0, j = 0;  // j: of the chain
+            uint32_t phase = 0, acc_phase = 0, turn_phase = 0;
             for (int64_t t = pair; t < tiles && ok; t += pairs) {
-                for (int k0 = 0; k0 < nk && ok; k0 += chain) {
-                    if (again && !mbar_wait_bounded(&acc_empty[b], acc_phase ^ 1u)) {
-                        ok = false;
-                        break;
+                for (int k0 = 0; k0 < nk && ok; k0 += chain, ++j) {
+                    const int b = j & 1, k1 = min(nk, k0 + chain);
+                    if (C::kIssuers == 1 && b != x) {
+                        const int to = s + k1 - k0, round = to / C::kStages;
+                        s = to - round * C::kStages, phase ^= (uint32_t)round & 1u;
+                        continue;
                     }
+                    if (j >= 2) {
+                        ok = mbar_wait_spin(&acc_empty[b], acc_phase);
+                        if (C::kIssuers == 1 || b == 1) acc_phase ^= 1u;
+                    }
+                    // the other issuer has seen every stage before this chain's, so that none is a phase behind
+                    if (C::kIssuers == 1 && j > 0) {
+                        ok = ok && mbar_wait_spin(&turn[x], turn_phase);
+                        turn_phase ^= 1u;
+                    }
+                    if (!ok) break;
                     tc::fence_after();
-                    const uint32_t d = tbase + (uint32_t)((b * C::kIssuers + x) * BN);
-                    const int k1 = min(nk, k0 + chain);
-                    for (int k = k0 + x; k < k1; k += C::kIssuers) {
-                        if (!mbar_wait_spin(&full[s], phase)) {
-                            ok = false;
-                            break;
-                        }
+                    const uint32_t d = tbase + (uint32_t)((C::kIssuers == 1 ? x : 2 * b + x) * BN);
+                    int k = k0 + (C::kIssuers == 2 ? x : 0);
+                    auto multiply = [&] {
                         tc::fence_after();
                         const uint64_t da = desc + (uint64_t)(s * (C::kStageBytes >> 4)), db = da + (128 * 128 >> 4);
 #pragma unroll
                         for (int i = 0; i < kKStep / 16; ++i)
-                            tc::mma_pair(d, da + 2 * i, db + 2 * i, idesc, k > k0 + x || i > 0);
+                            tc::mma_pair(d, da + 2 * i, db + 2 * i, idesc, k >= k0 + C::kIssuers || i > 0);
                         tc::commit_pair(&empty[s]);
                         s += C::kIssuers;
                         if (s >= C::kStages) s -= C::kStages, phase ^= 1u;
+                    };
+                    for (; k < (C::kIssuers == 1 ? k1 - 1 : k1); k += C::kIssuers) {
+                        if (!mbar_wait_spin(&full[s], phase)) {
+                            ok = false;
+                            break;
+                        }
+                        multiply();
+                    }
+                    if (C::kIssuers == 1) {  // the last step: the other issuer may go on
+                        ok = ok && mbar_wait_spin(&full[s], phase);
+                        mbar_arrive(&turn[x ^ 1]);
+                        if (!ok) break;
+                        multiply();
                     }
                     tc::commit_pair(&acc_full[b]);
-                    if (++b == 2) b = 0, acc_phase ^= 1u, again = true;
                 }
             }
         }
@@ -652,7 +691,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
         using V = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
         constexpr int kChunk = 64 / SZ;  // outputs in a staging row
         constexpr int kHalf = kOut / 2;  // outputs of this warp
-        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int q = warp & 3, half = (warp - 4) >> 2;  // lanes 32 q .. of tensor memory
         uint8_t* stage = staging + (warp - 4) * 2048;
         float* bias = s_bias + (warp - 4) * (BN / 2);  // [0, kHalf): of the outputs (the gate's); then the up projection's
         const int row = lane >> 2, piece = lane & 3;   // of the 16-byte moves: rows row + 8 i
@@ -683,18 +722,27 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 if (whole(0)) fetch(0);
                 else move_values<V, false>(stage, const_cast<void*>(e.residual), e.ldr, m, n0, e.M, e.N, lane);
             }
-            // the chains before the last one: [0, kHalf) of the outputs (the gate's), then the up projection's
-            float sum[SZ == 4 ? BN / 2 : 1];
-            if constexpr (SZ == 4) {
+            // [0, kHalf) of the outputs (the gate's), then the up projection's
+            float sum[CHAINED ? BN / 2 : 1];
+            auto ready = [&] {
+                if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                tc::fence_after();
+                return tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::kIssuers * BN + half * kHalf);
+            };
+            auto release = [&] {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::peer_arrive(tc::peer_addr(smem_u32(&acc_empty[b]), 0));
+                if (++b == 2) b = 0, phase ^= 1u;
+            };
+            if constexpr (CHAINED) {
 #pragma unroll
                 for (int i = 0; i < BN / 2; ++i) sum[i] = 0.0f;
 #pragma unroll 1
-                for (int k0 = 0; k0 + chain < nk; k0 += chain) {
-                    if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
-                    ok = __all_sync(0xffffffffu, ok);
+                for (int k0 = 0; k0 < nk; k0 += chain) {
+                    const uint32_t acc = ready();
                     if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::kIssuers * BN + half * kHalf);
 #pragma unroll
                     for (int g = 0; g < BN / 2; g += 16) {
                         uint32_t v[C::kIssuers][16];
@@ -709,17 +757,11 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                             for (int i = 0; i < 16; ++i) sum[g + i] += __uint_as_float(v[x][i]);
                         }
                     }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::peer_arrive(tc::peer_addr(smem_u32(&acc_empty[b]), 0));
-                    if (++b == 2) b = 0, phase ^= 1u;
+                    release();
                 }
             }
-            if (!mbar_wait_bounded(&acc_full[b], phase)) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            tc::fence_after();
-            const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::kIssuers * BN + half * kHalf);
-#pragma unroll(SZ == 4 ? kHalf / kChunk : 1)  // 16-bit: the activations' code once; float32: sum[] is registers
+            const uint32_t acc = CHAINED ? 0u : ready();
+#pragma unroll 1  // the activations' code once
             for (int c = 0; c < kHalf; c += kChunk) {
                 if (!ok) break;
                 if (n0 + c >= e.N || m >= e.M) break;
@@ -735,31 +777,38 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                     __syncwarp();
                 }
                 float f[kChunk], up[kChunk];
+                if constexpr (CHAINED) {
 #pragma unroll
-                for (int h = 0; h < kChunk; h += 16) {
-                    uint32_t v[C::kIssuers][16], u[C::kIssuers][16];
-#pragma unroll
-                    for (int x = 0; x < C::kIssuers; ++x) {
-                        tc::tmem_load16(acc + (uint32_t)(x * BN + c + h), v[x]);
-                        if (GATED) tc::tmem_load16(acc + (uint32_t)(x * BN + kOut + c + h), u[x]);
+                    for (int i = 0; i < kChunk; ++i) {
+                        f[i] = sum[i];
+                        up[i] = GATED ? sum[kHalf + i] : 0.0f;
                     }
-                    tc::tmem_wait();
+                    // registers have no index: the next chunk's move up
 #pragma unroll
-                    for (int x = 0; x < C::kIssuers; ++x) {
-                        tc::tmem_ready(v[x]);
-                        if (GATED) tc::tmem_ready(u[x]);
-                    }
+                    for (int i = 0; i < BN / 2 - kChunk; ++i) sum[i] = sum[i + kChunk];
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        f[h + i] = __uint_as_float(v[0][i]);
-                        up[h + i] = GATED ? __uint_as_float(u[0][i]) : 0.0f;
-                        if constexpr (C::kIssuers == 2) {
-                            f[h + i] += __uint_as_float(v[1][i]);
-                            if (GATED) up[h + i] += __uint_as_float(u[1][i]);
+                    for (int h = 0; h < kChunk; h += 16) {
+                        uint32_t v[C::kIssuers][16], u[C::kIssuers][16];
+#pragma unroll
+                        for (int x = 0; x < C::kIssuers; ++x) {
+                            tc::tmem_load16(acc + (uint32_t)(x * BN + c + h), v[x]);
+                            if (GATED) tc::tmem_load16(acc + (uint32_t)(x * BN + kOut + c + h), u[x]);
                         }
-                        if constexpr (SZ == 4) {
-                            f[h + i] += sum[c + h + i];
-                            if (GATED) up[h + i] += sum[kHalf + c + h + i];
+                        tc::tmem_wait();
+#pragma unroll
+                        for (int x = 0; x < C::kIssuers; ++x) {
+                            tc::tmem_ready(v[x]);
+                            if (GATED) tc::tmem_ready(u[x]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            f[h + i] = __uint_as_float(v[0][i]);
+                            up[h + i] = GATED ? __uint_as_float(u[0][i]) : 0.0f;
+                            if constexpr (C::kIssuers == 2) {
+                                f[h + i] += __uint_as_float(v[1][i]);
+                                if (GATED) up[h + i] += __uint_as_float(u[1][i]);
+                            }
                         }
                     }
                 }
@@ -811,10 +860,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
                 }
                 __syncwarp();
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::peer_arrive(tc::peer_addr(smem_u32(&acc_empty[b]), 0));
-            if (++b == 2) b = 0, phase ^= 1u;
+            if (!CHAINED) release();
         }
     }
     if (!ok && lane == 0) set_status(&g_status, MPE_STATUS_WAIT_TIMEOUT);
@@ -884,7 +930,7 @@ cudaError_t launch_narrow(const mpe_linear_args& p, const Epilogue& e, cudaStrea
     cfg.numAttrs = 2;
     const int nk = (p.K + kKStep - 1) / kKStep;
     return cudaLaunchKernelEx(&cfg, k_narrow<NT, S, GATED>, mw, mx, e, nk,
-                              p.out_type == MPE_TYPE_F32 ? kChain / kKStep : nk, tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
+                              chain_of(type_bytes(p.out_type)) / kKStep, tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
 }
 
 template <int NT, bool GATED>
@@ -907,15 +953,23 @@ cudaError_t launch_narrow_for(const mpe_linear_args& p, const Epilogue& e, int n
     }
 }
 
-template <int BN, bool GATED, int SZ>
+template <int BN, bool GATED, int SZ, bool CHAINED>
 cudaError_t launch_wide(const mpe_linear_args& p, const Epilogue& e, int sms, cudaStream_t st) {
-    using C = Wide<BN>;
+    using C = Wide<BN, CHAINED>;
     alignas(64) CUtensorMap mx, mw;
     const int64_t wrows = GATED ? 2 * (int64_t)p.N : p.N;
     if (!encode(&mx, p.x, p.type, p.M, p.K, p.ldx, 128) || !encode(&mw, p.w, p.type, wrows, p.K, p.ldw, BN / 2))
         return cudaErrorInvalidValue;
-    cudaError_t err = cudaFuncSetAttribute(k_wide<BN, GATED, SZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t err = cudaFuncSetAttribute(k_wide<BN, GATED, SZ, CHAINED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (err != cudaSuccess) return err;
+    if constexpr (CHAINED) {
+        // a block that starts with fewer registers than it shares out would wait for ever
+        static const bool enough = [] {
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, k_wide<BN, GATED, SZ, CHAINED>) == cudaSuccess && a.numRegs == C::kRegs;
+        }();
+        if (!enough) return cudaErrorLaunchOutOfResources;
+    }
     constexpr int kOut = GATED ? BN / 2 : BN;
     const Tiles g{(p.M + kTileM - 1) / kTileM, (p.N + kOut - 1) / kOut};
     const int64_t tiles = (int64_t)g.m * g.n;
@@ -933,16 +987,21 @@ cudaError_t launch_wide(const mpe_linear_args& p, const Epilogue& e, int sms, cu
     cfg.numAttrs = 2;
     // steps for every issuer alike: a box past K reads as zeros
     const int nk = (p.K + kKStep - 1) / kKStep, steps = (nk + C::kIssuers - 1) / C::kIssuers * C::kIssuers;
-    return cudaLaunchKernelEx(&cfg, k_wide<BN, GATED, SZ>, mx, mw, e, g, steps,
+    return cudaLaunchKernelEx(&cfg, k_wide<BN, GATED, SZ, CHAINED>, mx, mw, e, g, steps,
                               tc::instr_desc(kTileM, BN, p.type == MPE_TYPE_BF16));
 }
 
+template <int BN, int SZ>
+cudaError_t launch_wide_as(const mpe_linear_args& p, const Epilogue& e, int sms, cudaStream_t st) {
+    if (p.K > Wide<BN, true>::kIssuers * chain_of(SZ))
+        return p.gated ? launch_wide<BN, true, SZ, true>(p, e, sms, st) : launch_wide<BN, false, SZ, true>(p, e, sms, st);
+    return p.gated ? launch_wide<BN, true, SZ, false>(p, e, sms, st) : launch_wide<BN, false, SZ, false>(p, e, sms, st);
+}
+
 cudaError_t launch_wide_for(const mpe_linear_args& p, const Epilogue& e, int bn, int sms, cudaStream_t st) {
-    // float32: the sums of earlier chains are registers, which takes the narrower tile
-    if (p.out_type == MPE_TYPE_F32)
-        return p.gated ? launch_wide<128, true, 4>(p, e, sms, st) : launch_wide<128, false, 4>(p, e, sms, st);
-    if (bn == 128) return p.gated ? launch_wide<128, true, 2>(p, e, sms, st) : launch_wide<128, false, 2>(p, e, sms, st);
-    return p.gated ? launch_wide<256, true, 2>(p, e, sms, st) : launch_wide<256, false, 2>(p, e, sms, st);
+    // float32: the narrower tile, whose results' chunks are as many
+    if (p.out_type == MPE_TYPE_F32) return launch_wide_as<128, 4>(p, e, sms, st);
+    return bn == 128 ? launch_wide_as<128, 2>(p, e, sms, st) : launch_wide_as<256, 2>(p, e, sms, st);
 }
 
 // The kernel for a product: k_wide<tile> (wide) or k_narrow<tile, split>.

@@ -98,6 +98,20 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// ---- registers ----
+// All four warps of a warpgroup: R registers a thread (a multiple of 8) from here on.
+// What some give up others may take, within what the block was launched with.
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void more_registers() {
+    __syncwarp();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 // ---- thread-block clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
