@@ -315,8 +315,9 @@ __device__ __noinline__ int rank_exact(const SelectArgs& a, const T* row, int e0
 // of 1 ulp: below 2^-21. Adding the bias rounds by 2^-24 |key|. Keys (or sums of
 // two) further apart than the errors of both are in float64's order. Of nearer
 // keys, which a sigmoid with a bias has in one row of 1000, the order is found
-// again from their float64 values; rows with near groups, a NaN or an infinity
-// in the way take select_exact.
+// again from their float64 values (rank_exact), and which groups stay where those
+// are near (groups_exact); rows with a NaN, or with too few keys above -inf, take
+// select_exact.
 constexpr int kSelWarps = 4;
 
 // The two largest values of several, in order (no NaN).
@@ -598,10 +599,12 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
         for (int i = 1; i < EPL; ++i) top = fmaxf(top, key[i]);
         if (!exact && 3 * __popc(__ballot_sync(kFull, top != -INFINITY)) >= 4 * a.k) {
             float best, edge = nth_top(top, a.k, best);
-            if (edge != -INFINITY) {
+            const float tol = a.bias ? 2.0f * err + 0x1p-22f * fmaxf(fabsf(best), fabsf(edge)) : 0.0f;
+            edge -= tol;
+            // -inf (or NaN) also when the largest key is +inf, or the k-th near the lowest float: padding and
+            // dropped groups would reach that
+            if (edge > -INFINITY) {
                 __syncwarp();  // the last row's are read
-                const float tol = a.bias ? 2.0f * err + 0x1p-22f * fmaxf(fabsf(best), fabsf(edge)) : 0.0f;
-                edge -= tol;
                 int count = 0;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) count += key[i] >= edge;
