@@ -562,10 +562,10 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
                 push2(m1, m2, o1);
                 m2 = fmaxf(m2, o2);
             }
-            float mine = m1, big = 0.0f;  // the group's score; |key| + |key| in a finite sum
+            float mine = m1, big = 0.0f;  // the group's score; |key| + |key| of finite keys (infinite: past float32)
             if (sums && gs > 1) {
                 mine = m1 + m2;
-                big = isfinite(mine) ? fabsf(m1) + fabsf(m2) : 0.0f;
+                big = isfinite(m1) && isfinite(m2) ? fabsf(m1) + fabsf(m2) : 0.0f;
             }
             if (group >= a.n_groups) mine = -INFINITY;
             // every group's score once, in the first of its lanes
@@ -582,9 +582,11 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
             }
             exact |= __any_sync(kFull, mine != mine);
             if (sums || a.bias) {
-                // the last group kept against the first one dropped
+                // The last group kept against the first one dropped. Where no finite keys' sum is past float32,
+                // infinite scores are what they seem, and equal ones stay in the groups' order
                 const float over = warp_top(in ? -INFINITY : mine);
-                if (!exact && least - over <= 4.0f * err + 0x1p-22f * fmaxf(warp_top(big), fabsf(over)))
+                big = warp_top(big);
+                if (!exact && (big == INFINITY || least - over <= 4.0f * err + 0x1p-22f * fmaxf(big, fabsf(over))))
                     in = groups_exact<T>(a, row, lane, group, e0, n, (double)m);
             }
 #pragma unroll

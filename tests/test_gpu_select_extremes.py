@@ -71,3 +71,31 @@ def test_infinite_biases_in_groups(mpe, E, G, keep, k, score):
     g = torch.Generator().manual_seed(E * G)
     for b in biases(E, g):
         check(mpe, torch.randn(5, E, generator=g) * 1.5, k, b, score, n_groups=G, keep_groups=keep, group_score="max")
+
+
+@pytest.mark.parametrize("E,G,keep,k", [(4, 2, 1, 2), (14, 7, 3, 3), (30, 10, 7, 5), (32, 8, 3, 4), (32, 32, 8, 8), (31, 31, 9, 2),
+                                        (20, 2, 1, 4), (32, 4, 2, 8), (6, 3, 2, 3), (64, 8, 3, 6), (256, 8, 4, 8), (512, 16, 5, 8)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_sums_of_two_past_float32(mpe, E, G, keep, k, score):
+    """Sums of a group's two largest keys that only float64 holds, beside true infinities."""
+    g = torch.Generator().manual_seed(E * G + 1)
+    more = []
+    for values in ((2e38, 2e38, 3e38, 3e38), (-2e38, -3e38, -3.4e38), (-MAX, -INF), (MAX, 3e38, 2e38, -INF)):
+        more.append(torch.tensor(values)[torch.randint(0, len(values), (E,), generator=g)])
+    # one usable expert in some groups, all barred by the lowest float in others
+    b = torch.full((E,), -MAX)
+    b[::3] = -INF
+    more.append(b)
+    # whole groups barred, which is common: the rest by their scores
+    b = torch.randn(E, generator=g) * 0.1
+    b[E // G * ((G + 1) // 2):] = -INF
+    more.append(b)
+    for b in biases(E, g) + more:
+        with np.errstate(invalid="ignore"):  # inf - inf in a group's sum: NaN, which ranks lowest
+            check(mpe, torch.randn(5, E, generator=g) * 1.5, k, b, score, n_groups=G, keep_groups=keep)
+
+
+def test_the_larger_of_two_sums_past_float32(mpe):
+    b = torch.tensor([2e38, 2e38, 3e38, 3e38])
+    check(mpe, torch.zeros(3, 4), 2, b, "sigmoid", n_groups=2, keep_groups=1)
+    check(mpe, torch.zeros(3, 4), 2, -b.flip(0), "sigmoid", n_groups=2, keep_groups=1)
