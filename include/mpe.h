@@ -606,7 +606,8 @@ typedef struct mpe_select_args {
  * scale s_e / (sum of the chosen s) with renormalize. Without a bias the order
  * (of groups by MPE_GROUP_MAX too) is the logits' own.
  * The choice is that of float64 scores and keys: float32 ones decide
- * wherever they are further apart than their error. Weights are float32.
+ * wherever they are further apart than their error. Weights are float32, summed
+ * in the order of choice. The same input gives the same bits.
  * A logit of -inf has score 0 (masked), a bias of -inf bars an expert until
  * nothing else is left, and a token whose chosen scores are all 0 gets weights
  * 0 (with ids, as everywhere, in [0, E)). A NaN logit, or +inf under the

@@ -361,11 +361,13 @@ __device__ __forceinline__ float nth_top(float v, int n, float& best) {
     return r;
 }
 
-// Token t's ids and weights: a lane with `chosen` has the expert `id` of logit l
-// (-inf in the others) that is number `rank`; lm is the largest chosen logit, m and
-// inv the softmax's maximum and 1 / sum where weights are not divided by their own.
-__device__ __forceinline__ void write_chosen(const SelectArgs& a, int t, bool chosen, int rank, int id, float l, float lm,
-                                             bool broken, bool softmax, float m, float inv) {
+// Token t's ids and weights: lane j < k has the expert `id` that is number j, of logit
+// l (-inf in the other lanes), so that the sum's order is the experts' rank; lm is the
+// largest chosen logit, m and inv the softmax's maximum and 1 / sum where weights are
+// not divided by their own.
+__device__ __forceinline__ void write_chosen(const SelectArgs& a, int t, int lane, int id, float l, float lm, bool broken,
+                                             bool softmax, float m, float inv) {
+    const bool chosen = lane < a.k;
     float s = 0.0f;
     if (a.renorm) {  // of the chosen logits alone
         if (chosen && l != -INFINITY) {
@@ -379,8 +381,8 @@ __device__ __forceinline__ void write_chosen(const SelectArgs& a, int t, bool ch
         s = a.scale * (softmax ? (l == -INFINITY ? 0.0f : expf(l - m) * inv) : 1.0f / (1.0f + expf(-l)));
     }
     if (chosen) {
-        a.ids[(size_t)t * a.k + rank] = id;
-        a.w[(size_t)t * a.k + rank] = broken ? NAN : s;
+        a.ids[(size_t)t * a.k + lane] = id;
+        a.w[(size_t)t * a.k + lane] = broken ? NAN : s;
     }
 }
 
@@ -456,8 +458,7 @@ __global__ void __launch_bounds__(32 * kSelWarps) k_select16(const SelectArgs a)
             sum = warp_sum(sum);
             inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
         }
-        const bool chosen = lane < a.k;
-        write_chosen(a, t, chosen, lane, (int)(kIndexBits - (mine & kIndexBits)), chosen ? logit(mine) : -INFINITY, lm, broken,
+        write_chosen(a, t, lane, (int)(kIndexBits - (mine & kIndexBits)), lane < a.k ? logit(mine) : -INFINITY, lm, broken,
                      softmax, lm, inv);
     }
 }
@@ -692,9 +693,16 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
             l = as_float(row[id]);
             rank = lane;
         }
-        const bool chosen = rank < a.k;
-        if (!chosen) l = -INFINITY;
-        write_chosen(a, t, chosen, rank, id, l, warp_top(l), broken, softmax, m, inv);
+        // to the lane of its rank: places among the candidates came in any order
+        __syncwarp();
+        if (rank < a.k) {
+            s_key[warp][rank] = l;
+            s_id[warp][rank] = id;
+        }
+        __syncwarp();
+        l = lane < a.k ? s_key[warp][lane] : -INFINITY;
+        id = s_id[warp][lane];
+        write_chosen(a, t, lane, id, l, warp_top(l), broken, softmax, m, inv);
     }
 }
 
