@@ -49,12 +49,14 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 // One warp: `cols` (a power of two, 32 .. 512) tensor-memory columns.
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
                  "r"(cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
 __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
 }
 
@@ -120,6 +122,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 // All threads of the cluster; what was written before is visible after.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();  // the whole warp at once, also after loops that its threads leave one by one
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The address of shared address `a` in CTA `rank` of the cluster.
@@ -159,12 +162,14 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
         : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t cols) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
                  "r"(cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 __device__ __forceinline__ void tmem_free_pair(uint32_t base, uint32_t cols) {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
 }
 // load_box into this CTA's shared memory, its bytes counted on rank 0's barrier
