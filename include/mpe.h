@@ -673,10 +673,11 @@ typedef struct mpe_linear_args {
  *   out = act(x w^T + bias) + residual, or, gated,
  *   out = act(x wg^T + bg) (x wu^T + bu) + residual,
  * products accumulated and the epilogue computed in fp32, rounded once to
- * out_type. The same input gives the same bits. An accumulator takes n = 512
- * inputs (16-bit out_type: 1024), where the tensor cores cut instead of rounding,
- * and such sums are added in fp32: one over K is off by at most
- * n/16 2^-23 + (K/n + 10) 2^-24 of the sum of its terms' magnitudes.
+ * out_type. The same input gives the same bits. An accumulator takes at most
+ * n = 512 inputs (16-bit out_type: 2048), where the tensor cores cut instead of
+ * rounding, and such sums are added in fp32: one over K is off by at most
+ * n/16 2^-23 + (K/512 + 10) 2^-24 of the sum of its terms' magnitudes (16-bit:
+ * K/1024).
  * x and w are 16-byte aligned with ldx and ldw multiples of 8 (a pitch of one
  * row is not read and may be anything); bias, residual and out are aligned to
  * their elements; ldx, ldw >= K, ldr, ldo >= N. `residual` may be `out` itself

@@ -208,6 +208,10 @@ constexpr int kRows = 128;
 // 14336); 1024 for a 16-bit one, whose half step is 250 times what they lose, so that
 // the share of K that a CTA of k_narrow has is most often one chain.
 __host__ __device__ constexpr int chain_of(int out_bytes) { return out_bytes == 4 ? 512 : 1024; }
+// In k_wide the first chain of a 16-bit result is twice as long: the epilogue of the
+// tile before runs beside it (4096 x 4096 x 4096 with bias, silu and residual: 116 us
+// with 1024 inputs, 110 with 2048, 106 with one chain).
+__host__ __device__ constexpr int first_chain(int out_bytes) { return out_bytes == 4 ? 512 : 2048; }
 
 template <int NT>
 struct Narrow {
@@ -474,12 +478,12 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
 //   warps 4-11 epilogue, 32 tokens and half of the outputs each: a thread has a
 //              token's outputs, which go through 2 KB of shared memory a warp, so
 //              that global memory is read and written in runs of 64 bytes of a row
-// CHAINED (K beyond one chain of chain_of() inputs an accumulator): the epilogue warps
+// CHAINED (K beyond one chain of first_chain() inputs an accumulator): the epilogue warps
 // add every chain to sums in registers, 128 a thread with BN 256: warps 0-3 leave
 // theirs to warps 4-11 (setmaxnreg). The accumulator is free again before the
-// epilogue begins. Against one chain that costs 3% of the time (8192 x 2 x 2048 x
-// 7168 gated: 322 -> 332 us, 4096 x 4096 x 4096: 99 -> 103), 5% where one round of
-// tiles leaves the epilogue uncovered (2048 x 2048 x 7168: 46.5 -> 48.8); chains of
+// epilogue begins. Against one chain that costs 3 to 4% of the time (8192 x 2 x 2048 x
+// 7168 gated: 317 -> 326 us, 4096 x 4096 x 4096: 98 -> 102), 5% where one round of
+// tiles leaves the epilogue uncovered (2048 x 2048 x 7168: 47.0 -> 49.6); chains of
 // 2048 inputs would cost 0.7% less.
 template <int BN, bool CHAINED>
 struct Wide {
@@ -563,6 +567,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
     uint64_t* acc_full = empty + C::kStages;                          // each CTA: [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by both CTAs' epilogue warps
     const int chain = CHAINED ? C::kIssuers * chain_of(SZ) / kKStep : nk;  // steps of all issuers
+    const int chain0 = CHAINED ? C::kIssuers * first_chain(SZ) / kKStep : nk;
     uint64_t* turn = acc_empty + 2;                                   // rank 0: [2] an issuer's chain is next
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -639,8 +644,9 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
             int s = C::kIssuers == 2 ? x : 0, j = 0;  // j: of the chain
             uint32_t phase = 0, acc_phase = 0, turn_phase = 0;
             for (int64_t t = pair; t < tiles && ok; t += pairs) {
-                for (int k0 = 0; k0 < nk && ok; k0 += chain, ++j) {
-                    const int b = j & 1, k1 = min(nk, k0 + chain);
+                for (int k0 = 0, k1; k0 < nk && ok; k0 = k1, ++j) {
+                    const int b = j & 1;
+                    k1 = min(nk, k0 + (k0 == 0 ? chain0 : chain));
                     if (C::kIssuers == 1 && b != x) {
                         const int to = s + k1 - k0, round = to / C::kStages;
                         s = to - round * C::kStages, phase ^= (uint32_t)round & 1u;
@@ -740,7 +746,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
 #pragma unroll
                 for (int i = 0; i < BN / 2; ++i) sum[i] = 0.0f;
 #pragma unroll 1
-                for (int k0 = 0; k0 < nk; k0 += chain) {
+                for (int k0 = 0; k0 < nk; k0 += k0 == 0 ? chain0 : chain) {
                     const uint32_t acc = ready();
                     if (!ok) break;
 #pragma unroll
@@ -993,7 +999,7 @@ cudaError_t launch_wide(const mpe_linear_args& p, const Epilogue& e, int sms, cu
 
 template <int BN, int SZ>
 cudaError_t launch_wide_as(const mpe_linear_args& p, const Epilogue& e, int sms, cudaStream_t st) {
-    if (p.K > Wide<BN, true>::kIssuers * chain_of(SZ))
+    if (p.K > Wide<BN, true>::kIssuers * first_chain(SZ))
         return p.gated ? launch_wide<BN, true, SZ, true>(p, e, sms, st) : launch_wide<BN, false, SZ, true>(p, e, sms, st);
     return p.gated ? launch_wide<BN, true, SZ, false>(p, e, sms, st) : launch_wide<BN, false, SZ, false>(p, e, sms, st);
 }

@@ -2,11 +2,11 @@
 
 The tensor cores cut what they add to an accumulator: an instruction of 16 inputs loses less than one unit
 of the accumulator's last place, 2^-23 of it, always towards zero. An accumulator takes 512 inputs (float32
-results; 32 instructions) or 1024 (16-bit results; 64), then it starts again and its sum is added up in float32,
-rounding to nearest: 2^-24 an addition, at most one for every such run of inputs, one for every two issuers' and
-one for every rank's. So a sum of terms of one sign is off by at most
+results; 32 instructions) or 1024, the first time up to 2048 (16-bit results; 128), then it starts again and its
+sum is added up in float32, rounding to nearest: 2^-24 an addition, at most one for every such run of inputs, one
+for every two issuers' and one for every rank's. So a sum of terms of one sign is off by at most
 
-    n 2^-23 + (K / inputs + 10) 2^-24,   n = 32 or 64,
+    n 2^-23 + (K / inputs + 10) 2^-24,   n = 32 and inputs = 512, or n = 128 and inputs = 1024,
 
 of itself, and one of both signs by that much of the sum of magnitudes. A 16-bit result is rounded once: half a
 step of the result's binade."""
@@ -26,8 +26,8 @@ def mpe():
 
 
 def bound(K, out):
-    inputs = 512 if out == "f32" else 1024
-    return inputs / 16 * 2.0 ** -23 + (K / inputs + 10) * 2.0 ** -24
+    n, inputs = (32, 512) if out == "f32" else (128, 1024)
+    return n * 2.0 ** -23 + (K / inputs + 10) * 2.0 ** -24
 
 
 def half_step(v, out):
