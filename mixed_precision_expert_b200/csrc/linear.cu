@@ -40,23 +40,33 @@ __device__ __forceinline__ float sigmoid(float v) {
     return r;
 }
 
-// The normal distribution function, (1 + erf(v / sqrt 2)) / 2, by the rational
-// approximation of erf in Abramowitz and Stegun, 7.1.26: off by at most 7.5e-8.
+// The normal distribution function. EXACT, for float32 results: erfc(-v / sqrt 2) / 2
+// (8192 x 2048 x 768 with bias, gelu and residual: 81 us, 61 with the other). Else, for
+// x = |v| and t = 1 / (1 + 0.36 x), the tail is t P(t) e^(-x^2 / 2): P is the polynomial
+// of degree 6 with the least relative error over x = 0 .. 14, found by reweighted least
+// squares (8.8e-7). In float32: 1.2e-6 near 0, and 0.7 x^2 2^-24 from the exponent's
+// argument, 8.4e-6 at x = 13. (Abramowitz and Stegun 7.1.26, which has the same form,
+// bounds the absolute error alone, which is 26% of the tail at x = 5; the same product
+// with a bf16 result: 42.6 us with it, 43.2 with P.)
+template <bool EXACT>
 __device__ __forceinline__ float normal_cdf(float v) {
+    if (EXACT) return 0.5f * erfcf(-0.70710678f * v);
     float t, e;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f * 0.70710678f, fabsf(v), 1.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.36f, fabsf(v), 1.0f)));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-0.72134752f * v * v));
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(t, p, 1.421413741f);
-    p = fmaf(t, p, -0.284496736f);
-    p = fmaf(t, p, 0.254829592f);
-    const float q = 0.5f * t * p * e;
+    float p = fmaf(t, 0.0470559f, -0.17976336f);
+    p = fmaf(t, p, 0.18095219f);
+    p = fmaf(t, p, 0.026550535f);
+    p = fmaf(t, p, 0.13971885f);
+    p = fmaf(t, p, 0.14177252f);
+    p = fmaf(t, p, 0.14371304f);
+    const float q = t * p * e;
     return v < 0.0f ? q : 1.0f - q;
 }
 
 // The activation of V values: the choice is outside the loop, so that the code of
 // each stands here once a call.
-template <int V>
+template <int V, bool EXACT>
 __device__ __forceinline__ void activate(float (&v)[V], int act) {
     if (act == MPE_ACT_SILU) {
 #pragma unroll
@@ -67,7 +77,7 @@ __device__ __forceinline__ void activate(float (&v)[V], int act) {
         for (int i = 0; i < V; ++i) v[i] *= sigmoid(1.59576912f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
     } else if (act == MPE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= normal_cdf(v[i]);
+        for (int i = 0; i < V; ++i) v[i] *= normal_cdf<EXACT>(v[i]);
     } else if (act == MPE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
@@ -167,7 +177,8 @@ struct Output {
                 if (GATED) u[i] += bu[i];
             }
         }
-        activate<V>(v, e.act);
+        if (e.out_type == MPE_TYPE_F32) activate<V, true>(v, e.act);
+        else activate<V, false>(v, e.act);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (GATED) v[i] *= u[i];
@@ -822,7 +833,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) f[i] += bias[c + i];
                 }
-                activate<kChunk>(f, e.act);
+                activate<kChunk, SZ == 4>(f, e.act);
                 if (GATED) {
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) f[i] *= up[i] + (e.bias ? bias[kHalf + c + i] : 0.0f);

@@ -12,7 +12,7 @@ import math
 
 import numpy as np
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def activate(v: np.ndarray, act: str) -> np.ndarray:
@@ -22,7 +22,7 @@ def activate(v: np.ndarray, act: str) -> np.ndarray:
         if act == "silu":
             return v / (1.0 + np.exp(-v))
         if act == "gelu":
-            return 0.5 * v * (1.0 + _erf(v / math.sqrt(2.0)))
+            return 0.5 * v * _erfc(-v / math.sqrt(2.0))  # 1 + erf would cancel far below 0
         if act == "gelu_tanh":
             return 0.5 * v * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (v + 0.044715 * v ** 3)))
     assert act == "none", act
