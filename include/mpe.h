@@ -678,7 +678,10 @@ typedef struct mpe_linear_args {
  * rounding, and such sums are added in fp32: one over K is off by at most
  * n/16 2^-23 + (K/512 + 10) 2^-24 of the sum of its terms' magnitudes (16-bit:
  * K/1024).
- * MPE_ACT_GELU is off by at most (32 + 1.3 v^2) 2^-24 of itself, in the tail too.
+ * Activations are off relative to themselves, in the tails too, by at most
+ * (32 + 1.3 v^2) 2^-24 (gelu), 10 2^-24 (silu; 16-bit out_type: 9 + 2.4 |v|) and,
+ * with z = 1.6 (v + 0.044715 v^3), 6 |z| 2^-24 more than silu at z (gelu_tanh), as
+ * long as they are normal in float32.
  * x and w are 16-byte aligned with ldx and ldw multiples of 8 (a pitch of one
  * row is not read and may be anything); bias, residual and out are aligned to
  * their elements; ldx, ldw >= K, ldr, ldo >= N. `residual` may be `out` itself

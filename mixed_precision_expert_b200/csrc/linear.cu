@@ -31,9 +31,15 @@ __device__ __forceinline__ float load_as_float(const void* p, size_t i, int type
     return __half2float(static_cast<const __half*>(p)[i]);
 }
 
-// 1 / (1 + e^-v): the exponential is off by (2 + 1.2 |v|) ulp, which costs the result
-// at most 2^-22 since s (1 - s) <= e^-|v|
+// 1 / (1 + e^-v). EXACT, for float32 results: expf, and for either sign from e^-|v|. Else
+// the fast exponential, which is off by (2 + 1.2 |v|) ulp: 1.2e-5 at most before the
+// result underflows, a twentieth of fp16's half step.
+template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float v) {
+    if (EXACT) {
+        const float e = expf(-fabsf(v));
+        return __fdividef(v < 0.0f ? e : 1.0f, 1.0f + e);
+    }
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * v));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
@@ -70,11 +76,11 @@ template <int V, bool EXACT>
 __device__ __forceinline__ void activate(float (&v)[V], int act) {
     if (act == MPE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i]);
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid<EXACT>(v[i]);
     } else if (act == MPE_ACT_GELU_TANH) {
         // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= sigmoid(1.59576912f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid<EXACT>(1.59576912f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
     } else if (act == MPE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] *= normal_cdf<EXACT>(v[i]);

@@ -24,7 +24,8 @@ def activate(v: np.ndarray, act: str) -> np.ndarray:
         if act == "gelu":
             return 0.5 * v * _erfc(-v / math.sqrt(2.0))  # 1 + erf would cancel far below 0
         if act == "gelu_tanh":
-            return 0.5 * v * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (v + 0.044715 * v ** 3)))
+            # (1 + tanh z) / 2 = 1 / (1 + e^-2z), which does not cancel
+            return v / (1.0 + np.exp(-math.sqrt(8.0 / math.pi) * (v + 0.044715 * v ** 3)))
     assert act == "none", act
     return v
 

@@ -7,7 +7,8 @@ units of u = 2^-24 of the value:
             moves it by at most v^2 + 1 times that; two products: 1.3 v^2 + 12.
             16-bit: the fit 15 u, rcp and ex2 (1 and 2 ulp) 6 u, nine roundings of the polynomial and products, the
             exponent's argument, v^2 / 2 with two roundings and a constant's (2.3 u): 1.2 v^2 + 31.
-  silu      float32: e^-|v| (2 ulp) in numerator and denominator 4 + 2 u, a sum, a quotient, a product: 10.
+  silu      float32: e^-|v| (2 ulp, 4 u) moves e / (1 + e) by 1 / (1 + e) and 1 / (1 + e) by e / (1 + e) times that, 4 u
+            at most; a sum 1 u, a quotient (2 ulp) 4 u, a product 1 u: 10.
             16-bit: the exponential 2 + 1.2 |v| ulp, rcp 1 ulp, a sum, a product: 2.4 |v| + 9.
   gelu_tanh as silu at z = 2 sqrt(2 / pi) (v + 0.044715 v^3), whose six roundings move the result by |z| each at most.
 
@@ -77,7 +78,7 @@ def run(mpe, act, out, N, K, gated):
     assert not bad.any(), (int(bad.sum()), v[bad][:5], ref[bad][:5], got.cpu()[bad][:5])
 
 
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["gelu", "silu", "gelu_tanh"])
 @pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("N,K,gated", [(4, 16, False), (5, 16, False), (512, 64, False), (1028, 64, True)])
 def test_relative_to_the_value(mpe, act, out, N, K, gated):
