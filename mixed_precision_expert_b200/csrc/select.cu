@@ -729,8 +729,8 @@ cudaError_t launch_select_t(const SelectArgs& a, int epl, int sms, cudaStream_t 
 }
 
 // Experts a lane has when `groups` groups of gs get `lanes` lanes each, a power of
-// two: the fewest that fit the warp (at most 64: E <= 1024, and at least 16 lanes
-// are in use).
+// two: the fewest that fit the warp (at most 64, at E <= 1024: 17 groups of 60 have a
+// lane each).
 int experts_per_lane(int groups, int gs, int* lanes) {
     for (int epl = 1;; epl *= 2) {
         int n = 1;
@@ -766,7 +766,9 @@ constexpr int kImpWarps = 16, kImpCluster = 8;
 // where rows are not aligned to that). A lane copies its pieces of the rows to come
 // asynchronously into its own part of shared memory, so that enough rows are on
 // their way to keep memory busy while a row's maximum and sum go round the warp.
-// The fast exponential: 2 + 1.2 d ulp for a score of e^-d.
+// The fast exponential, off by 2 + 1.2 d ulp for a score of e^-d: what a mean consists
+// of are its rows' large scores (65536 x 256: error against float64 2.8e-8, 2.7e-8 with
+// float32's own exponential in torch). With expf: 65536 x 256 float32 14.4 -> 17.1 us.
 template <typename T, int EPL>
 struct ImpRing {
     static constexpr int kRowBytes = 32 * EPL * (int)sizeof(T);
