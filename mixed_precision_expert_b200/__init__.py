@@ -240,26 +240,33 @@ _ops = None  # see _load_ops
 _torch = None
 
 
+def _queries(torch):
+    """(current device, current stream of a device), as numbers: what torch.cuda's
+    current_device() and current_stream() wrap, at a twentieth of their time, or those where
+    a torch lacks them."""
+    C = torch._C
+    return (getattr(C, "_cuda_getDevice", None) or torch.cuda.current_device,
+            getattr(C, "_cuda_getCurrentRawStream", None)
+            or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+
+
 def _load_ops():
     """(torch's types by MPE_TYPE_*, current device, current stream of a device, the three
-    calls): the two queries are what torch.cuda.current_device() and current_stream() wrap, at
-    a twentieth of their time."""
+    calls)."""
     global _ops, _torch
     import torch
     _torch = torch
     torch.cuda.current_device()  # initialises CUDA
     L = lib()
-    _ops = ({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16},
-            torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+    _ops = ({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}, *_queries(torch),
             L.mpe_select_experts, L.mpe_expert_importance, L.mpe_linear)
     return _ops
 
 
 def _on(dev: int, f, args: bytes):
     """f(args, stream) for a device other than the current one."""
-    import torch
-    with torch.cuda.device(dev):
-        return f(args, torch._C._cuda_getCurrentRawStream(dev))
+    with _torch.cuda.device(dev):
+        return f(args, _ops[2](dev))
 
 
 def _device(t) -> int:
