@@ -1,6 +1,7 @@
 // out = act(x w^T + bias) + residual and its gated form (mpe_linear).
 #include <cuda.h>
 
+#include <atomic>
 #include <cstdio>
 #include <cstring>
 #include <type_traits>
@@ -987,11 +988,14 @@ cudaError_t launch_wide(const mpe_linear_args& p, const Epilogue& e, int sms, cu
     if (err != cudaSuccess) return err;
     if constexpr (CHAINED) {
         // a block that starts with fewer registers than it shares out would wait for ever
-        static const bool enough = [] {
+        static std::atomic<bool> enough{false};
+        if (!enough) {
             cudaFuncAttributes a;
-            return cudaFuncGetAttributes(&a, k_wide<BN, GATED, SZ, CHAINED>) == cudaSuccess && a.numRegs == C::kRegs;
-        }();
-        if (!enough) return cudaErrorLaunchOutOfResources;
+            err = cudaFuncGetAttributes(&a, k_wide<BN, GATED, SZ, CHAINED>);
+            if (err != cudaSuccess) return err;
+            if (a.numRegs != C::kRegs) return cudaErrorLaunchOutOfResources;
+            enough = true;
+        }
     }
     constexpr int kOut = GATED ? BN / 2 : BN;
     const Tiles g{(p.M + kTileM - 1) / kTileM, (p.N + kOut - 1) / kOut};
