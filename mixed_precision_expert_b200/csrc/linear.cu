@@ -1039,7 +1039,7 @@ struct Choice {
 
 // The form with the least estimated time, in us, from times measured on B200 over
 // M 1 .. 8192, N 16 .. 14336, K 64 .. 14336 (of 60 products at random the form taken
-// is within 10% of the best of all forms for 53, at worst 1.4 times it):
+// is within 10% of the best of all forms for 56, at worst 1.3 times it):
 //   k_narrow<NT>  starts and ends in 3.3 + 0.025 NT (one tile, K = 2048, split 8: 3.8
 //                 with NT 16, 4.1, 4.9 and 6.9 with 128); a step takes a CTA 0.24, or
 //                 what an SM takes in at 105 GB/s where it has several CTAs (NT

@@ -390,9 +390,9 @@ __device__ __forceinline__ void write_chosen(const SelectArgs& a, int t, int lan
 // The logit's 19 bits (sign, exponent and 10 bits of bf16 or f16 as a float, in an
 // order-preserving form) and the expert's index below them are one integer that no
 // other expert has: a lane sorts its own, and the warp's largest is taken k times,
-// which settles ties, infinities and NaN on the way. Up to 128 experts: 8192 x 128
-// bf16 5.4 us, and 8.6 with k_select, whose threshold takes any key; 32768 x 128
-// 16.8 and 24.5; but 32768 x 256 31.3 and 26.4, since a lane moves its keys up k times.
+// which settles ties, infinities and NaN on the way. Up to 128 experts (on the device):
+// 8192 x 128 bf16 5.2 us, and 8.6 with k_select, whose threshold takes any key; 32768 x
+// 128 16.8 and 24.3; but 32768 x 256 31.3 and 25.7, since a lane moves its keys up k times.
 constexpr uint32_t kIndexBits = 0x1FFFu;  // above MPE_MAX_EXPERTS
 
 // In 1 comparison for 2 keys, 5 for 4.
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, EPL <= 8 ? 8 : EPL == 16 ? 5 :
     const int n = group * gs < a.E ? max(0, min(EPL, gs - from)) : 0;
     const float err = softmax ? (EPL + 24) * 0x1p-24f : 0x1p-21f;
     // the bias stays in registers, or, where there are too many, in shared memory
-    // by lanes (16 a lane from global memory a row: 32768 x 512 in 77 us instead of 50)
+    // by lanes (16 a lane from global memory a row: 32768 x 512 in 77 us instead of 45)
     constexpr bool kHold = EPL <= 8;
     float held[kHold ? EPL : 1];
     __shared__ float s_bias[kHold ? 1 : 32 * EPL];
