@@ -217,19 +217,20 @@ struct Output {
 //   all        sums over the ranks, epilogue
 // The tensor cores cut what they add to an accumulator instead of rounding it: the
 // error grows by about 10^-9 of the result a value of K, always towards zero
-// (measured: 1.6e-5 at K = 14336). So an accumulator starts again every chain_of()
+// (measured: 1.6e-5 at K = 14336). So an accumulator starts again every first_chain()
 // inputs, and warps 4-7 add the chains up in registers, rounding to nearest.
 constexpr int kKStep = 64;
 constexpr int kRows = 128;
 
 // Inputs that an accumulator takes: 512 for a float32 result (error 4.8e-7 at K =
-// 14336); 1024 for a 16-bit one, whose half step is 250 times what they lose, so that
-// the share of K that a CTA of k_narrow has is most often one chain.
-__host__ __device__ constexpr int chain_of(int out_bytes) { return out_bytes == 4 ? 512 : 1024; }
-// In k_wide the first chain of a 16-bit result is twice as long: the epilogue of the
-// tile before runs beside it (4096 x 4096 x 4096 with bias, silu and residual: 116 us
-// with 1024 inputs, 110 with 2048, 106 with one chain).
+// 14336). For a 16-bit one, whose half step is 120 times what 2048 inputs lose, 2048 in
+// k_narrow, so that a CTA's share of K is most often one chain, which all warps read at
+// its end (512 x 2048 x 7168: 18.2 us, 21.2 with 1024), and in the first chain of
+// k_wide, beside which the epilogue of the tile before runs (4096 x 4096 x 4096 with
+// bias, silu and residual: 116 us with 1024 inputs, 110 with 2048, 106 with one chain);
+// 1024 in k_wide's next ones.
 __host__ __device__ constexpr int first_chain(int out_bytes) { return out_bytes == 4 ? 512 : 2048; }
+__host__ __device__ constexpr int next_chain(int out_bytes) { return out_bytes == 4 ? 512 : 1024; }
 
 template <int NT>
 struct Narrow {
@@ -584,7 +585,7 @@ k_wide(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
     uint64_t* empty = full + C::kStages;                              // each CTA: its stage was multiplied
     uint64_t* acc_full = empty + C::kStages;                          // each CTA: [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;                               // rank 0: [2] read by both CTAs' epilogue warps
-    const int chain = CHAINED ? C::kIssuers * chain_of(SZ) / kKStep : nk;  // steps of all issuers
+    const int chain = CHAINED ? C::kIssuers * next_chain(SZ) / kKStep : nk;  // steps of all issuers
     const int chain0 = CHAINED ? C::kIssuers * first_chain(SZ) / kKStep : nk;
     uint64_t* turn = acc_empty + 2;                                   // rank 0: [2] an issuer's chain is next
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
@@ -954,7 +955,7 @@ cudaError_t launch_narrow(const mpe_linear_args& p, const Epilogue& e, cudaStrea
     cfg.numAttrs = 2;
     const int nk = (p.K + kKStep - 1) / kKStep;
     return cudaLaunchKernelEx(&cfg, k_narrow<NT, S, GATED>, mw, mx, e, nk,
-                              chain_of(type_bytes(p.out_type)) / kKStep, tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
+                              first_chain(type_bytes(p.out_type)) / kKStep, tc::instr_desc(kRows, NT, p.type == MPE_TYPE_BF16));
 }
 
 template <int NT, bool GATED>
