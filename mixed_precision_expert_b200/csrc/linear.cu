@@ -500,10 +500,11 @@ k_narrow(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUte
 // CHAINED (K beyond one chain of first_chain() inputs an accumulator): the epilogue warps
 // add every chain to sums in registers, 128 a thread with BN 256: warps 0-3 leave
 // theirs to warps 4-11 (setmaxnreg). The accumulator is free again before the
-// epilogue begins. Against one chain that costs 3 to 4% of the time (8192 x 2 x 2048 x
-// 7168 gated: 317 -> 326 us, 4096 x 4096 x 4096: 98 -> 102), 5% where one round of
-// tiles leaves the epilogue uncovered (2048 x 2048 x 7168: 47.0 -> 49.6); chains of
-// 2048 inputs would cost 0.7% less.
+// epilogue begins. Against one chain that costs 2.5 us where a last round of tiles
+// leaves the epilogue uncovered (1024 x 4096 x 4096 with bias, silu and residual: 29.8
+// -> 32.5 us, 2048 x 2048 x 7168 with bias and gelu: 45.2 -> 47.7), 2 to 4% of many
+// rounds (4096 x 4096 x 4096: 96 -> 100, 8192 x 4096 x 14336: 642 -> 656); chains of 2048
+// inputs throughout would cost 0.7% less.
 template <int BN, bool CHAINED>
 struct Wide {
     static constexpr int kStageBytes = 128 * 128 + BN / 2 * 128;
